@@ -1,0 +1,612 @@
+// decay.cu -- decay attention (heads that forget at a constant rate): the C entries, the
+// chunked walk on CUDA cores and the recurrent step.
+#include "decay.h"
+
+#include "tc_common.cuh"
+
+namespace gla {
+namespace {
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ float from_f<float>(float x) {
+  return x;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+
+// ============================================================================
+// The walk on CUDA cores.  A chunk of C tokens, m of them live:
+//     o_i = sum_{j<=i} lambda^{i-j} (x_i . y_j) z_j + lambda^{i+1} x_i S ,
+//     S  <- lambda^m S + sum_j lambda^{m-1-j} y_j^T z_j ,
+// all weights at most one.  A reverse walk takes the chunks and the tokens of a chunk
+// backwards and carries S' = lambda R, so that a start state enters its first token
+// undecayed and the final state is dL/dS_0 itself: j >= i, lambda^{m-1-i} x_i S',
+// S' <- lambda^m S' + sum_j lambda^{j+1} y_j^T z_j.
+//
+// CTA = (64 columns of V, segment, sequence and head), 256 threads as 16 x 16; x, y, z,
+// the scores and the state live in shared memory in fp32.  Every product is a register
+// tile per thread (4 x 4 at C = 64) fed by 16-byte shared-memory reads: rows 16 apart per
+// thread and a row stride of 4 mod 32 words keep those free of bank conflicts.  Bound by
+// fp32 arithmetic and shared-memory reads, not by HBM.
+// ============================================================================
+constexpr int kThreads = 256;
+constexpr int kBV = 64;
+
+template <int C, int K>
+struct CcSmem {
+  static constexpr int KS = K + 4;
+  static constexpr int PS = C + 4;
+  static constexpr int x = 0, y = x + C * KS, z = y + C * KS, s = z + C * kBV, p = s + K * kBV, w = p + C * PS;
+  static constexpr int floats = w + C + 1 + 3;
+};
+
+// rows [0, m) x columns [c0, c0 + n) of a token-strided matrix into [C][stride], zeros around them
+template <typename T, int C>
+__device__ __forceinline__ void load_tile(float *dst, int stride, int width, const T *src, long st, int m, int n) {
+  for (int e = threadIdx.x; e < C * (width / 4); e += kThreads) {
+    const int r = e / (width / 4), c = 4 * (e % (width / 4));
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < m) {
+      const T *p = src + r * st + c;
+      if (c < n) v.x = to_f(p[0]);
+      if (c + 1 < n) v.y = to_f(p[1]);
+      if (c + 2 < n) v.z = to_f(p[2]);
+      if (c + 3 < n) v.w = to_f(p[3]);
+    }
+    *reinterpret_cast<float4 *>(dst + r * stride + c) = v;
+  }
+}
+
+template <typename T, int C, int K, bool OUT>
+__global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
+  using L = CcSmem<C, K>;
+  extern __shared__ __align__(16) float sm[];
+  float *X = sm + L::x, *Y = sm + L::y, *Z = sm + L::z, *S = sm + L::s, *Pm = sm + L::p, *W = sm + L::w;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int tiles = (w.V + kBV - 1) / kBV;
+  const int vt = blockIdx.x % tiles, seg = blockIdx.y;
+  const long bh = blockIdx.x / tiles;
+  const int b = (int)(bh / w.H), h = (int)(bh % w.H), v0 = vt * kBV;
+  const dev::DSeq sq = dev::decay_seq(w, b);
+  const int n = (sq.len + C - 1) / C, nseg = max(1, (n + w.L - 1) / w.L);
+  if (seg >= nseg || (!OUT && seg == nseg - 1)) return;
+  int i0, i1;
+  dev::decay_slots(w.s0, w.s1, w.alias, w.nseq, b, OUT ? w.status : nullptr, i0, i1);
+  const double rate = dev::decay_rate(w.ld, h, w.status);
+  for (int i = tid; i <= C; i += kThreads) W[i] = (float)dev::decay_pow(rate, i);
+
+  // ---- start state: thread (ty, tx) owns rows 4 ty + 64 i + e, columns 4 tx .. +3
+  const long KV = (long)w.K * w.V;
+  float *wsb = w.ws + bh * w.P * KV;
+  const bool pass = w.P > 1 && nseg > 1;  // states come from and go to ws
+  const float far = (float)dev::decay_pow(rate, (long)w.L * C);
+#pragma unroll 1
+  for (int i = 0; i < K / 64 + (K % 64 ? 1 : 0); ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int k = 4 * ty + 64 * i + e;
+      if (k >= K) continue;
+      float4 v4;
+      float *v = &v4.x;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int vc = v0 + 4 * tx + c;
+        float a = 0.f;
+        if (k < w.K && vc < w.V) {
+          if (OUT && pass) {
+            // entry 0: the start state (segment 0); entries 1 .. seg: states of the segments before
+            const float *u = wsb + (long)k * w.V + vc;
+            if (seg == 0) {
+              a = u[0];
+            } else {
+              for (int j = 1; j <= seg; ++j) a = fmaf(a, far, u[j * KV]);
+            }
+          } else if (seg == 0 && i0 >= 0) {
+            a = w.s0.p[i0 * w.s0.slot + h * w.s0.head + k * w.s0.row + vc * w.s0.col];
+            if (!OUT) wsb[(long)k * w.V + vc] = a;
+          } else if (!OUT && seg == 0) {
+            wsb[(long)k * w.V + vc] = 0.f;
+          }
+        }
+        v[c] = a;
+      }
+      *reinterpret_cast<float4 *>(S + k * kBV + 4 * tx) = v4;
+    }
+
+  const T *x = (const T *)w.x.p + sq.b * w.x.sb + h * w.x.sh + sq.row0 * w.x.st;
+  const T *y = (const T *)w.y.p + sq.b * w.y.sb + h * w.y.sh + sq.row0 * w.y.st;
+  const T *z = (const T *)w.z.p + sq.b * w.z.sb + h * w.z.sh + sq.row0 * w.z.st + v0;
+  const int nv = min(kBV, w.V - v0);
+  const long rows = w.packed ? w.T : (long)w.nseq * w.T;
+  const int i_end = min(n, (seg + 1) * w.L);
+  for (int i = seg * w.L; i < i_end; ++i) {
+    const int c = w.reverse ? n - 1 - i : i;
+    const long t0 = (long)c * C;
+    const int m = (int)min((long)C, sq.len - t0);
+    __syncthreads();
+    if (OUT) load_tile<T, C>(X, L::KS, K, x + t0 * w.x.st, w.x.st, m, w.K);
+    load_tile<T, C>(Y, L::KS, K, y + t0 * w.y.st, w.y.st, m, w.K);
+    load_tile<T, C>(Z, kBV, kBV, z + t0 * w.z.st, w.z.st, m, nv);
+    __syncthreads();
+    constexpr int R = C / 16;
+    if (OUT) {
+      float s[R][R];
+#pragma unroll
+      for (int a = 0; a < R; ++a)
+#pragma unroll
+        for (int d = 0; d < R; ++d) s[a][d] = 0.f;
+#pragma unroll 2
+      for (int k = 0; k < K; k += 4) {
+        float4 xv[R], yv[R];
+#pragma unroll
+        for (int a = 0; a < R; ++a) xv[a] = *reinterpret_cast<const float4 *>(X + (ty + 16 * a) * L::KS + k);
+#pragma unroll
+        for (int a = 0; a < R; ++a) yv[a] = *reinterpret_cast<const float4 *>(Y + (tx + 16 * a) * L::KS + k);
+#pragma unroll
+        for (int a = 0; a < R; ++a)
+#pragma unroll
+          for (int d = 0; d < R; ++d) {
+            s[a][d] = fmaf(xv[a].x, yv[d].x, s[a][d]);
+            s[a][d] = fmaf(xv[a].y, yv[d].y, s[a][d]);
+            s[a][d] = fmaf(xv[a].z, yv[d].z, s[a][d]);
+            s[a][d] = fmaf(xv[a].w, yv[d].w, s[a][d]);
+          }
+      }
+#pragma unroll
+      for (int a = 0; a < R; ++a)
+#pragma unroll
+        for (int d = 0; d < R; ++d) {
+          const int t = ty + 16 * a, u = tx + 16 * d, g = w.reverse ? u - t : t - u;
+          Pm[t * L::PS + u] = g >= 0 ? s[a][d] * W[g] : 0.f;
+        }
+      __syncthreads();
+      float4 in[R], ia[R];
+#pragma unroll
+      for (int a = 0; a < R; ++a) in[a] = ia[a] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int k = 0; k < K; ++k) {
+        const float4 sv = *reinterpret_cast<const float4 *>(S + k * kBV + 4 * tx);
+#pragma unroll
+        for (int a = 0; a < R; ++a) {
+          const float q = X[(ty + 16 * a) * L::KS + k];
+          in[a].x = fmaf(q, sv.x, in[a].x);
+          in[a].y = fmaf(q, sv.y, in[a].y);
+          in[a].z = fmaf(q, sv.z, in[a].z);
+          in[a].w = fmaf(q, sv.w, in[a].w);
+        }
+      }
+#pragma unroll 4
+      for (int u = 0; u < C; ++u) {
+        const float4 zv = *reinterpret_cast<const float4 *>(Z + u * kBV + 4 * tx);
+#pragma unroll
+        for (int a = 0; a < R; ++a) {
+          const float q = Pm[(ty + 16 * a) * L::PS + u];
+          ia[a].x = fmaf(q, zv.x, ia[a].x);
+          ia[a].y = fmaf(q, zv.y, ia[a].y);
+          ia[a].z = fmaf(q, zv.z, ia[a].z);
+          ia[a].w = fmaf(q, zv.w, ia[a].w);
+        }
+      }
+#pragma unroll
+      for (int a = 0; a < R; ++a) {
+        const int t = ty + 16 * a;
+        if (t >= m) continue;
+        const float f = W[w.reverse ? m - 1 - t : t + 1];
+        const float r[4] = {fmaf(f, in[a].x, ia[a].x), fmaf(f, in[a].y, ia[a].y), fmaf(f, in[a].z, ia[a].z),
+                            fmaf(f, in[a].w, ia[a].w)};
+        T *o = (T *)w.o.p + sq.b * w.o.sb + h * w.o.sh + (sq.row0 + t0 + t) * w.o.st + v0;
+        const long row = w.packed ? sq.row0 + t0 + t : (long)b * w.T + t0 + t;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (4 * tx + e >= nv) continue;
+          float val = r[e];
+          float *part = w.acc + ((long)h * rows + row) * w.V + v0 + 4 * tx + e;
+          if (w.acc_in) val += *part;
+          if (w.acc_out) *part = val;
+          else o[4 * tx + e] = from_f<T>(val);
+        }
+      }
+      __syncthreads();  // S and Z are read
+    }
+    for (int e = tid; e < C * kBV; e += kThreads) {
+      const int u = e / kBV;
+      if (u < m) Z[e] *= W[w.reverse ? u + 1 : m - 1 - u];
+    }
+    __syncthreads();
+    const float dm = W[m];
+#pragma unroll 1
+    for (int i4 = 0; i4 < (K + 63) / 64; ++i4) {
+      const int k0 = 4 * ty + 64 * i4;
+      if (K % 64 != 0 && k0 >= K) continue;
+      float4 d[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        d[e] = *reinterpret_cast<const float4 *>(S + (k0 + e) * kBV + 4 * tx);
+        d[e].x *= dm, d[e].y *= dm, d[e].z *= dm, d[e].w *= dm;
+      }
+      float4 f[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int u = 0; u < C; ++u) {
+        const float4 yv = *reinterpret_cast<const float4 *>(Y + u * L::KS + k0);
+        const float4 zv = *reinterpret_cast<const float4 *>(Z + u * kBV + 4 * tx);
+        const float q[4] = {yv.x, yv.y, yv.z, yv.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          f[e].x = fmaf(q[e], zv.x, f[e].x);
+          f[e].y = fmaf(q[e], zv.y, f[e].y);
+          f[e].z = fmaf(q[e], zv.z, f[e].z);
+          f[e].w = fmaf(q[e], zv.w, f[e].w);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<float4 *>(S + (k0 + e) * kBV + 4 * tx) =
+            make_float4(d[e].x + f[e].x, d[e].y + f[e].y, d[e].z + f[e].z, d[e].w + f[e].w);
+    }
+  }
+
+  // ---- the state after the segment: to ws, or to the pool after the sequence's last
+  const bool last = seg == nseg - 1;
+  if (!OUT || (last && i1 >= 0)) {
+#pragma unroll 1
+    for (int i = 0; i < (K + 63) / 64; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int k = 4 * ty + 64 * i + e;
+        if (k >= w.K || k >= K) continue;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int vc = v0 + 4 * tx + c;
+          if (vc >= w.V) continue;
+          const float a = S[k * kBV + 4 * tx + c];
+          if (!OUT) wsb[(seg + 1) * KV + (long)k * w.V + vc] = a;
+          else w.s1.p[i1 * w.s1.slot + h * w.s1.head + k * w.s1.row + vc * w.s1.col] = a;
+        }
+      }
+  }
+}
+
+template <typename T, int C, int K>
+int launch_cc(const DecayWalk &w, cudaStream_t st) {
+  const int smem = CcSmem<C, K>::floats * 4;
+  if (cudaFuncSetAttribute(k_decay_cc<T, C, K, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+      cudaFuncSetAttribute(k_decay_cc<T, C, K, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return GLA_ERR_CUDA;
+  const unsigned gx = (unsigned)((long)w.nseq * w.H * ((w.V + kBV - 1) / kBV));
+  if (w.P > 1)
+    GLA_LAUNCH(K_DECAY_STATES, st, (k_decay_cc<T, C, K, false><<<dim3(gx, w.P - 1), kThreads, smem, st>>>(w)));
+  GLA_LAUNCH(K_DECAY_WALK, st, (k_decay_cc<T, C, K, true><<<dim3(gx, w.P), kThreads, smem, st>>>(w)));
+  return GLA_OK;
+}
+
+template <typename T>
+int walk_cc(const DecayWalk &w, cudaStream_t st) {
+  if (w.K <= 64) return launch_cc<T, 64, 64>(w, st);
+  if (w.K <= 128) return launch_cc<T, 64, 128>(w, st);
+  return launch_cc<T, 32, 256>(w, st);
+}
+
+// ============================================================================
+// The recurrent step: one token per sequence.  Reads and rewrites the state once
+// (2 * 4 * dk * dv bytes a head) and is bound by HBM on it, or by latency where the batch
+// is small.  CTA = (kStepCols columns, sequence and head); a thread owns four columns and
+// every RG-th row, all of whose loads are issued before the first is used; the sums over
+// the rows go through shared memory.
+// ============================================================================
+template <typename T, int CQ>  // CQ: quads of columns per CTA
+__global__ void __launch_bounds__(256) k_decay_step(int H, int nseq, int K, int V, DView q, DView k, DView v, DView o,
+                                                    const float *ld, DPool s, unsigned *status) {
+  constexpr int RG = 256 / CQ;
+  __shared__ float sq[256], sk[256];
+  __shared__ float4 red[RG][CQ];
+  const int tid = threadIdx.x, jq = tid % CQ, rg = tid / CQ;
+  const int tiles = (V + 4 * CQ - 1) / (4 * CQ);
+  const int vt = blockIdx.x % tiles;
+  const long bh = blockIdx.x / tiles;
+  const int b = (int)(bh / H), h = (int)(bh % H);
+  int i0, i1;
+  const DPool none{};
+  dev::decay_slots(none, s, false, nseq, b, status, i0, i1);
+  if (i1 < 0) return;
+  const float lam = (float)dev::decay_pow(dev::decay_rate(ld, h, status), 1);
+  if (tid < K) {
+    sq[tid] = to_f(((const T *)q.p)[b * q.sb + h * q.sh + tid]);
+    sk[tid] = to_f(((const T *)k.p)[b * k.sb + h * k.sh + tid]);
+  }
+  __syncthreads();
+  const int col = vt * 4 * CQ + 4 * jq;
+  const T *vp = (const T *)v.p + b * v.sb + h * v.sh + col;
+  float *S = s.p + i1 * s.slot + h * s.head + col;
+  float vv[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) vv[e] = col + e < V ? to_f(vp[e]) : 0.f;
+  if (V % 4 == 0) {
+    if (col < V)
+#pragma unroll 8
+      for (int r = rg; r < K; r += RG) {
+        float4 *p = reinterpret_cast<float4 *>(S + (long)r * V);
+        float4 x = *p;
+        const float kr = sk[r], qr = sq[r];
+        x.x = fmaf(lam, x.x, kr * vv[0]);
+        x.y = fmaf(lam, x.y, kr * vv[1]);
+        x.z = fmaf(lam, x.z, kr * vv[2]);
+        x.w = fmaf(lam, x.w, kr * vv[3]);
+        *p = x;
+        acc[0] = fmaf(qr, x.x, acc[0]);
+        acc[1] = fmaf(qr, x.y, acc[1]);
+        acc[2] = fmaf(qr, x.z, acc[2]);
+        acc[3] = fmaf(qr, x.w, acc[3]);
+      }
+  } else {
+    for (int r = rg; r < K; r += RG)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (col + e < V) {
+          float *p = S + (long)r * V + e;
+          const float x = fmaf(lam, *p, sk[r] * vv[e]);
+          *p = x;
+          acc[e] = fmaf(sq[r], x, acc[e]);
+        }
+  }
+  red[rg][jq] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+  __syncthreads();
+  if (tid < 4 * CQ) {
+    const int c = vt * 4 * CQ + tid;
+    if (c < V) {
+      float sum = 0.f;
+#pragma unroll
+      for (int g = 0; g < RG; ++g) sum += (&red[g][tid / 4].x)[tid % 4];
+      ((T *)o.p)[b * o.sb + h * o.sh + c] = from_f<T>(sum);
+    }
+  }
+}
+
+}  // namespace
+
+bool decay_tc_takes(const DecayWalk &, int) { return false; }
+int decay_walk_tc(const DecayWalk &, cudaStream_t) { return GLA_ERR_UNSUPPORTED_SHAPE; }
+int decay_chunk_tc() { return 128; }
+
+int decay_chunk_cc(int K) { return K <= 128 ? 64 : 32; }
+
+int decay_walk_cc(const DecayWalk &w, int dtype, cudaStream_t st) {
+  return dtype == GLA_DTYPE_BF16 ? walk_cc<__nv_bfloat16>(w, st) : walk_cc<float>(w, st);
+}
+
+namespace {
+
+#define GLA_TRY(expr)            \
+  do {                           \
+    const int _r = (expr);       \
+    if (_r != GLA_OK) return _r; \
+  } while (0)
+
+constexpr int kPiece = 256;        // channels of one contraction
+constexpr int kMaxSegments = 32;
+constexpr long kMaxHeads = 1 << 20;
+
+int check_desc(const gla_decay_desc *d) {
+  if (!d) return GLA_ERR_INVALID_ARG;
+  if (d->B < 1 || d->H < 1 || d->T < 1 || d->dk < 1 || d->dv < 1 || d->segments < 0 || d->max_len < 0 ||
+      d->max_len > d->T) return GLA_ERR_INVALID_ARG;
+  if (d->dtype != GLA_DTYPE_BF16 && d->dtype != GLA_DTYPE_FP32) return GLA_ERR_INVALID_ARG;
+  if (d->dk > 256 || d->dv > 4096 || (long)d->B * d->H > kMaxHeads || d->segments > kMaxSegments)
+    return GLA_ERR_UNSUPPORTED_SHAPE;
+  return GLA_OK;
+}
+
+int check_view(const gla_view *v, int dtype, DView *out) {
+  if (!v || !v->data || v->sb < 0 || v->sh < 0 || v->st < 0) return GLA_ERR_INVALID_ARG;
+  if ((uintptr_t)v->data & (dtype == GLA_DTYPE_BF16 ? 1u : 3u)) return GLA_ERR_MISALIGNED;
+  *out = DView{v->data, (long)v->sb, (long)v->sh, (long)v->st};
+  return GLA_OK;
+}
+
+int check_states(const float *p) { return ((uintptr_t)p & 15u) ? GLA_ERR_MISALIGNED : GLA_OK; }
+
+DPool pool(const float *p, const int *idx, int slots, const gla_decay_desc *d, bool transposed) {
+  const long KV = (long)d->dk * d->dv;
+  return DPool{const_cast<float *>(p), idx, slots, d->H * KV, KV, transposed ? 1 : (long)d->dv,
+               transposed ? (long)d->dv : 1};
+}
+
+// Segments per sequence and chunks per segment of a walk.
+// Splitting reads y and z twice and passes states through memory, so a walk is split only
+// while it leaves SMs idle, and into segments of at least kMinChunks chunks.
+int most_segments(const gla_decay_desc *d, int max_len, int chunk, int V) {
+  constexpr int kMinChunks = 4;
+  const long lines = (long)d->B * d->H * ((V + kBV - 1) / kBV);
+  const int n = (max_len + chunk - 1) / chunk;
+  long p = d->segments ? d->segments : 148 / lines;
+  if (!d->segments && p > n / kMinChunks) p = n / kMinChunks;
+  if (p > kMaxSegments) p = kMaxSegments;
+  if (p > n) p = n;
+  return p < 1 ? 1 : (int)p;
+}
+void plan_segments(const gla_decay_desc *d, int max_len, int chunk, int V, int *P, int *L) {
+  const int p = most_segments(d, max_len, chunk, V), n = (max_len + chunk - 1) / chunk;
+  *L = (n + p - 1) / p;
+  *P = (n + *L - 1) / *L;
+}
+
+// bytes of ws: the state copies of the walk that needs most
+size_t ws_states(const gla_decay_desc *d) {
+  int most = 1;
+  for (int V : {d->dk, d->dv})
+    for (int chunk : {32, 64, 128}) {
+      const int p = most_segments(d, d->max_len ? d->max_len : d->T, chunk, V);
+      if (p > most) most = p;
+    }
+  return most > 1 ? align_up((size_t)d->B * d->H * most * d->dk * d->dv * sizeof(float), 256) : 0;
+}
+// partial outputs of a backward whose contraction over dv is taken in pieces
+size_t ws_acc(const gla_decay_desc *d) {
+  const size_t rows = d->max_len ? (size_t)d->T : (size_t)d->B * d->T;
+  return d->dv > kPiece ? align_up(rows * d->H * d->dk * sizeof(float), 256) : 0;
+}
+
+int check_ws(const gla_decay_desc *d, bool bwd) {
+  if (!d->workspace) return GLA_ERR_INVALID_ARG;
+  if ((uintptr_t)d->workspace & 255u) return GLA_ERR_MISALIGNED;
+  if (d->workspace_bytes < kStatusBytes + ws_states(d) + (bwd ? ws_acc(d) : 0)) return GLA_ERR_WORKSPACE_TOO_SMALL;
+  return GLA_OK;
+}
+
+// One walk, its contraction over K channels in pieces of at most kPiece.
+int run_walk(DecayWalk w, const gla_decay_desc *d, cudaStream_t st) {
+  const int K = w.K;
+  const long es = d->dtype == GLA_DTYPE_BF16 ? 2 : 4;
+  char *const x = (char *)w.x.p, *const y = (char *)w.y.p;
+  float *const s0 = w.s0.p;
+  const bool tc = decay_tc_takes(w, d->dtype);
+  for (int k0 = 0; k0 < K; k0 += kPiece) {
+    w.K = K - k0 < kPiece ? K - k0 : kPiece;
+    w.x.p = x + k0 * es;
+    w.y.p = y + k0 * es;
+    if (s0) w.s0.p = s0 + k0 * w.s0.row;
+    w.acc_in = k0 > 0;
+    w.acc_out = k0 + kPiece < K;
+    const int chunk = tc ? decay_chunk_tc() : decay_chunk_cc(w.K);
+    plan_segments(d, w.max_len, chunk, w.V, &w.P, &w.L);
+    GLA_TRY(tc ? decay_walk_tc(w, st) : decay_walk_cc(w, d->dtype, st));
+  }
+  return GLA_OK;
+}
+
+DecayWalk walk_base(const gla_decay_desc *d, const float *log_decay, const int *cu) {
+  DecayWalk w{};
+  w.nseq = d->B;
+  w.H = d->H;
+  w.T = d->T;
+  w.packed = cu != nullptr;
+  w.max_len = cu ? d->max_len : d->T;
+  w.ld = log_decay;
+  w.cu = cu;
+  w.status = (unsigned *)d->workspace;
+  w.ws = (float *)((char *)d->workspace + kStatusBytes);
+  w.acc = (float *)((char *)w.ws + ws_states(d));
+  return w;
+}
+
+int check_lengths(const gla_decay_desc *d, const int *cu) {
+  if ((cu != nullptr) != (d->max_len > 0)) return GLA_ERR_INVALID_ARG;
+  return (uintptr_t)cu & 3u ? GLA_ERR_MISALIGNED : GLA_OK;
+}
+
+}  // namespace
+}  // namespace gla
+
+using namespace gla;
+
+extern "C" {
+
+size_t gla_decay_workspace_size(const gla_decay_desc *desc, int for_bwd) {
+  if (check_desc(desc) != GLA_OK) return 0;
+  return kStatusBytes + ws_states(desc) + (for_bwd ? ws_acc(desc) : 0);
+}
+
+int gla_decay_fwd(const gla_decay_desc *desc, const gla_view *q, const gla_view *k, const gla_view *v,
+                  const float *log_decay, const int *cu_seqlens, const float *h0, const int *h0_index,
+                  const gla_view *o, float *h_final, const int *h_final_index, void *stream) {
+  GLA_TRY(check_desc(desc));
+  GLA_TRY(check_lengths(desc, cu_seqlens));
+  if (!log_decay || (h0_index && !h0) || (h_final_index && !h_final)) return GLA_ERR_INVALID_ARG;
+  if (h0 && (desc->slots0 < 1 || (!h0_index && desc->slots0 < desc->B))) return GLA_ERR_INVALID_ARG;
+  if (h_final && (desc->slots1 < 1 || (!h_final_index && desc->slots1 < desc->B))) return GLA_ERR_INVALID_ARG;
+  GLA_TRY(check_states(h0));
+  GLA_TRY(check_states(h_final));
+  GLA_TRY(check_ws(desc, false));
+  DecayWalk w = walk_base(desc, log_decay, cu_seqlens);
+  GLA_TRY(check_view(q, desc->dtype, &w.x));
+  GLA_TRY(check_view(k, desc->dtype, &w.y));
+  GLA_TRY(check_view(v, desc->dtype, &w.z));
+  GLA_TRY(check_view(o, desc->dtype, &w.o));
+  w.K = desc->dk;
+  w.V = desc->dv;
+  w.s0 = pool(h0, h0_index, desc->slots0, desc, false);
+  w.s1 = pool(h_final, h_final_index, desc->slots1, desc, false);
+  w.alias = h0 && h0 == h_final;
+  return run_walk(w, desc, (cudaStream_t)stream);
+}
+
+int gla_decay_bwd(const gla_decay_desc *desc, const gla_view *q, const gla_view *k, const gla_view *v,
+                  const float *log_decay, const int *cu_seqlens, const float *h0, const gla_view *do_,
+                  const float *dh_final, const gla_view *dq, const gla_view *dk, const gla_view *dv, float *dh0,
+                  void *stream) {
+  GLA_TRY(check_desc(desc));
+  GLA_TRY(check_lengths(desc, cu_seqlens));
+  if (!log_decay) return GLA_ERR_INVALID_ARG;
+  for (const float *s : {h0, dh_final, (const float *)dh0}) GLA_TRY(check_states(s));
+  GLA_TRY(check_ws(desc, true));
+  DView vq, vk, vv, vdo, vdq, vdk, vdv;
+  GLA_TRY(check_view(q, desc->dtype, &vq));
+  GLA_TRY(check_view(k, desc->dtype, &vk));
+  GLA_TRY(check_view(v, desc->dtype, &vv));
+  GLA_TRY(check_view(do_, desc->dtype, &vdo));
+  GLA_TRY(check_view(dq, desc->dtype, &vdq));
+  GLA_TRY(check_view(dk, desc->dtype, &vdk));
+  GLA_TRY(check_view(dv, desc->dtype, &vdv));
+  cudaStream_t st = (cudaStream_t)stream;
+  const DecayWalk base = walk_base(desc, log_decay, cu_seqlens);
+  const int B = desc->B;
+  DecayWalk w = base;  // dq = do S^T
+  w.K = desc->dv, w.V = desc->dk;
+  w.x = vdo, w.y = vv, w.z = vk, w.o = vdq;
+  w.s0 = pool(h0, nullptr, B, desc, true);
+  GLA_TRY(run_walk(w, desc, st));
+  w = base;  // dk = v R^T
+  w.reverse = 1;
+  w.K = desc->dv, w.V = desc->dk;
+  w.x = vv, w.y = vdo, w.z = vq, w.o = vdk;
+  w.s0 = pool(dh_final, nullptr, B, desc, true);
+  GLA_TRY(run_walk(w, desc, st));
+  w = base;  // dv = k R, dh0 = lambda R_1
+  w.reverse = 1;
+  w.K = desc->dk, w.V = desc->dv;
+  w.x = vk, w.y = vq, w.z = vdo, w.o = vdv;
+  w.s0 = pool(dh_final, nullptr, B, desc, false);
+  w.s1 = pool(dh0, nullptr, B, desc, false);
+  return run_walk(w, desc, st);
+}
+
+int gla_decay_step(const gla_decay_desc *desc, const gla_view *q, const gla_view *k, const gla_view *v,
+                   const float *log_decay, float *state, const int *index, const gla_view *o, void *stream) {
+  if (!desc) return GLA_ERR_INVALID_ARG;
+  gla_decay_desc d = *desc;
+  d.T = 1;
+  d.max_len = 0;
+  d.segments = 0;
+  GLA_TRY(check_desc(&d));
+  if (!log_decay || !state || d.slots1 < 1 || (!index && d.slots1 < d.B)) return GLA_ERR_INVALID_ARG;
+  GLA_TRY(check_states(state));
+  if ((uintptr_t)d.workspace & 3u) return GLA_ERR_MISALIGNED;
+  DView vq, vk, vv, vo;
+  GLA_TRY(check_view(q, d.dtype, &vq));
+  GLA_TRY(check_view(k, d.dtype, &vk));
+  GLA_TRY(check_view(v, d.dtype, &vv));
+  GLA_TRY(check_view(o, d.dtype, &vo));
+  const DPool s = pool(state, index, d.slots1, &d, false);
+  cudaStream_t st = (cudaStream_t)stream;
+  unsigned *status = (unsigned *)d.workspace;
+  constexpr int CQ = 16;
+  const long grid = (long)d.B * d.H * ((d.dv + 4 * CQ - 1) / (4 * CQ));
+  if (d.dtype == GLA_DTYPE_BF16)
+    GLA_LAUNCH(K_DECAY_STEP, st,
+               (k_decay_step<__nv_bfloat16, CQ><<<(unsigned)grid, 256, 0, st>>>(d.H, d.B, d.dk, d.dv, vq, vk, vv, vo,
+                                                                                log_decay, s, status)));
+  else
+    GLA_LAUNCH(K_DECAY_STEP, st,
+               (k_decay_step<float, CQ><<<(unsigned)grid, 256, 0, st>>>(d.H, d.B, d.dk, d.dv, vq, vk, vv, vo,
+                                                                        log_decay, s, status)));
+  return GLA_OK;
+}
+
+}  // extern "C"

@@ -14,7 +14,8 @@ const char *kernel_name(int id) {
       "f32_prep",     "f32_states",   "f32_scores",      "f32_out",    "f32_dstates",   "f32_dscores",
       "f32_dqk",      "f32_dv",       "f32_dg_out",      "tc_prep",    "tc_walk",       "tc_bwd",
       "status_clear", "decode",       "epilogue_fwd",    "epilogue_bwd", "epilogue_reduce", "state_scan",
-      "fold_segments", "f32_dlog_beta", "segment_starts", "tc_walk_epi"};
+      "fold_segments", "f32_dlog_beta", "segment_starts", "tc_walk_epi",
+      "decay_states", "decay_walk", "decay_step", "layernorm_fwd", "layernorm_bwd", "layernorm_reduce"};
   static_assert(sizeof(names) / sizeof(names[0]) == K_COUNT, "one name per KernelId");
   if (id < 0 || id >= K_COUNT) return "unknown";
   return names[id];
@@ -339,6 +340,7 @@ int gla_poll_status(const gla_desc *desc, void *stream) {
   if (cudaStreamSynchronize(st) != cudaSuccess) return GLA_ERR_CUDA;
   if (cudaMemsetAsync(desc->workspace, 0, sizeof(word), st) != cudaSuccess) return GLA_ERR_CUDA;
   if (word & (ST_TIMEOUT | ST_SMEM_ALIGN)) return GLA_ERR_TIMEOUT;
+  if (word & ST_INDEX) return GLA_ERR_INDEX;
   if (word & ST_GATE_RANGE) return GLA_ERR_GATE_RANGE;
   return GLA_OK;
 }
@@ -352,7 +354,8 @@ const char *gla_status_string(int code) {
     case GLA_ERR_WORKSPACE_TOO_SMALL: return "workspace too small";
     case GLA_ERR_CUDA: return "CUDA runtime error";
     case GLA_ERR_TIMEOUT: return "device-side bounded wait timed out";
-    case GLA_ERR_GATE_RANGE: return "gate decay too strong for the bf16 sub-chunk rescaling";
+    case GLA_ERR_GATE_RANGE: return "gate outside the supported range (too strong for the bf16 sub-chunk rescaling, or a decay above one)";
+    case GLA_ERR_INDEX: return "a sequence bound or state index out of range, or used twice";
     case GLA_ERR_NO_DEVICE: return "no sm_100 device for the bf16 tensor-core path";
     default: return "unknown status";
   }

@@ -33,6 +33,12 @@ enum KernelId : int {
   K_F32_DLB,
   K_SEG_STARTS,
   K_TC_WALK_EPI,
+  K_DECAY_STATES,
+  K_DECAY_WALK,
+  K_DECAY_STEP,
+  K_LN_FWD,
+  K_LN_BWD,
+  K_LN_REDUCE,
   K_COUNT
 };
 
@@ -56,7 +62,7 @@ struct Problem {
 };
 
 // Status word bits written by kernels into the workspace header.
-enum StatusBits : unsigned { ST_TIMEOUT = 1u, ST_GATE_RANGE = 2u, ST_SMEM_ALIGN = 4u };
+enum StatusBits : unsigned { ST_TIMEOUT = 1u, ST_GATE_RANGE = 2u, ST_SMEM_ALIGN = 4u, ST_INDEX = 8u };
 
 constexpr size_t kStatusBytes = 256;
 

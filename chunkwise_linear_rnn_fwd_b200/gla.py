@@ -21,7 +21,7 @@ GLA_OK = 0
 STATUS = {
     0: "GLA_OK", -1: "GLA_ERR_INVALID_ARG", -2: "GLA_ERR_UNSUPPORTED_SHAPE", -3: "GLA_ERR_MISALIGNED",
     -4: "GLA_ERR_WORKSPACE_TOO_SMALL", -5: "GLA_ERR_CUDA", -6: "GLA_ERR_TIMEOUT", -7: "GLA_ERR_GATE_RANGE",
-    -8: "GLA_ERR_NO_DEVICE",
+    -8: "GLA_ERR_NO_DEVICE", -9: "GLA_ERR_INDEX",
 }
 DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 GATE = {"vector": 0, "scalar": 1, "none": 2}
@@ -34,7 +34,8 @@ EXPORTS = ["gla_workspace_size", "gla_check", "gla_fwd", "gla_bwd", "gla_poll_st
            "gla_decode_step", "gla_selftest_timeout", "gla_epilogue_workspace_size", "gla_epilogue_fwd",
            "gla_epilogue_bwd", "gla_fwd_state", "gla_bwd_state", "gla_state_scan", "gla_general_workspace_size",
            "gla_fwd_general", "gla_bwd_general", "gla_poll_status_noalloc", "gla_last_cuda_error",
-           "gla_fwd_epilogue"]
+           "gla_fwd_epilogue", "gla_decay_workspace_size", "gla_decay_fwd", "gla_decay_bwd", "gla_decay_step",
+           "gla_layernorm_workspace_size", "gla_layernorm_fwd", "gla_layernorm_bwd"]
 
 
 class GLAError(RuntimeError):
@@ -51,6 +52,18 @@ class gla_desc(ctypes.Structure):
                 ("dv", ctypes.c_int), ("dtype", ctypes.c_int), ("gate", ctypes.c_int), ("subchunk", ctypes.c_int),
                 ("variant", ctypes.c_int), ("segments", ctypes.c_int), ("flags", ctypes.c_int),
                 ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+class gla_view(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("sb", ctypes.c_longlong), ("sh", ctypes.c_longlong),
+                ("st", ctypes.c_longlong)]
+
+
+class gla_decay_desc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("T", ctypes.c_int), ("max_len", ctypes.c_int),
+                ("dk", ctypes.c_int), ("dv", ctypes.c_int), ("dtype", ctypes.c_int), ("slots0", ctypes.c_int),
+                ("slots1", ctypes.c_int), ("segments", ctypes.c_int), ("workspace", ctypes.c_void_p),
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
@@ -101,6 +114,21 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gla_fwd_general.restype = i
     lib.gla_bwd_general.argtypes = [dp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, vp]
     lib.gla_bwd_general.restype = i
+    dd, vw, ll = ctypes.POINTER(gla_decay_desc), ctypes.POINTER(gla_view), ctypes.c_longlong
+    lib.gla_decay_workspace_size.argtypes = [dd, i]
+    lib.gla_decay_workspace_size.restype = ctypes.c_size_t
+    lib.gla_decay_fwd.argtypes = [dd, vw, vw, vw, vp, vp, vp, vp, vw, vp, vp, vp]
+    lib.gla_decay_fwd.restype = i
+    lib.gla_decay_bwd.argtypes = [dd, vw, vw, vw, vp, vp, vp, vw, vp, vw, vw, vw, vp, vp]
+    lib.gla_decay_bwd.restype = i
+    lib.gla_decay_step.argtypes = [dd, vw, vw, vw, vp, vp, vp, vw, vp]
+    lib.gla_decay_step.restype = i
+    lib.gla_layernorm_workspace_size.argtypes = [ll, i]
+    lib.gla_layernorm_workspace_size.restype = ctypes.c_size_t
+    lib.gla_layernorm_fwd.argtypes = [i, ll, i, vp, ll, vp, vp, f, vp, ll, vp, vp, vp]
+    lib.gla_layernorm_fwd.restype = i
+    lib.gla_layernorm_bwd.argtypes = [i, ll, i, vp, ll, vp, ll, vp, vp, vp, vp, ll, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.gla_layernorm_bwd.restype = i
     lib.gla_bwd.argtypes = [dp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, vp]
     lib.gla_bwd.restype = i
     lib.gla_poll_status.argtypes = [dp, vp]
@@ -511,6 +539,261 @@ def gla_bwd(q, k, v, log_alpha, do, h0=None, dh_final=None, *, chunk=64, gate=No
     if r != GLA_OK:
         raise GLAError(r, "gla_bwd")
     return dq, dk, dv, dlog_alpha, dh0
+
+
+def _on_device(fn):
+    """_on_stream, on the device of the first tensor: the library launches on the device
+    that is current, so a call with tensors of another device makes that one current."""
+    on_stream = _on_stream(fn)
+
+    @functools.wraps(fn)
+    def wrapper(x, *args, **kwargs):
+        if not x.is_cuda:
+            raise ValueError("tensors passed to the GLA library must be on a CUDA device")
+        stream = kwargs.get("stream")
+        if stream is not None and stream.device != x.device:
+            raise ValueError("stream and tensors are on different devices")
+        if x.device.index == torch.cuda.current_device():
+            return (fn if stream is None else on_stream)(x, *args, **kwargs)
+        with torch.cuda.device(x.device):
+            return on_stream(x, *args, **kwargs)
+    return wrapper
+
+
+def _like(t, name, dtype, shape, device):
+    """Refuse a tensor of another type, shape or device than the call needs."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} "
+                         f"on {t.device}")
+
+
+def _dense_ptr(t, name, dtype, shape, device):
+    if t is None:
+        return None
+    _like(t, name, dtype, shape, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _view(t, name, dtype, shape, device):
+    """gla_view of [B,H,T,d] (or [B,H,d]: one token) with contiguous channels."""
+    _like(t, name, dtype, shape, device)
+    s = t.stride()
+    if s[-1] != 1 and shape[-1] != 1:
+        raise ValueError(f"{name}: the channels of a token must be contiguous")
+    return ctypes.byref(gla_view(t.data_ptr(), s[0], s[1], s[2] if len(s) == 4 else 0))
+
+
+def _decay_desc(B, H, T, max_len, dk, dv, dtype, slots0=0, slots1=0, segments=0, workspace=None) -> gla_decay_desc:
+    if dtype not in DTYPE:
+        raise ValueError(f"unsupported dtype {dtype}")
+    d = gla_decay_desc(B, H, T, max_len, dk, dv, DTYPE[dtype], slots0, slots1, segments, None, 0)
+    if workspace is not None:
+        d.workspace, d.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return d
+
+
+def decay_workspace_size(B, H, T, dk, dv, dtype, for_bwd=False, *, max_len=0, segments=0) -> int:
+    """Bytes of workspace for gla_decay_fwd / gla_decay_bwd: B sequences of T tokens each
+    (dense) or, with max_len, B sequences of at most max_len tokens in T rows (packed)."""
+    d = _decay_desc(B, H, T, max_len, dk, dv, dtype, segments=segments)
+    n = load().gla_decay_workspace_size(ctypes.byref(d), int(for_bwd))
+    if n == 0:
+        raise GLAError(-2 if min(B, H, T, dk, dv) >= 1 and segments >= 0 else -1, "gla_decay_workspace_size")
+    return int(n)
+
+
+def alloc_decay_workspace(nbytes: int, device) -> torch.Tensor:
+    """A workspace for the decay calls with its status word cleared (read: poll_status)."""
+    ws = torch.empty(int(nbytes), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def _decay_setup(q, v, cu_seqlens, max_len, segments, workspace, for_bwd):
+    """(B sequences, max_len, cu pointer, workspace) of a chunked call.  A workspace the
+    caller did not pass lives for this call; nobody reads its status word."""
+    B, H, T, dk = q.shape
+    if cu_seqlens is None:
+        if max_len is not None:
+            raise ValueError("max_len goes with cu_seqlens")
+        cu, max_len = None, 0
+    else:
+        if B != 1:
+            raise ValueError("packed tensors are [1,H,T,d]")
+        if max_len is None:
+            raise ValueError("packed tensors need max_len, a bound on the longest sequence")
+        B = cu_seqlens.numel() - 1
+        cu = _dense_ptr(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), q.device)
+    if workspace is None:
+        workspace = torch.empty(decay_workspace_size(B, H, T, dk, v.shape[-1], q.dtype, for_bwd,
+                                                     max_len=max_len, segments=segments),
+                                dtype=torch.uint8, device=q.device)
+    return B, int(max_len), cu, workspace
+
+
+@_on_device
+def gla_decay_fwd(q, k, v, log_decay, *, cu_seqlens=None, max_len=None, h0=None, h0_index=None, o=None, h_final=None,
+                  h_final_index=None, want_final=True, segments=0, workspace=None, stream=None):
+    """Linear attention whose heads forget at a constant rate: S_t = lambda_h S_{t-1} + k_t^T v_t,
+    o_t = q_t S_t, lambda_h = exp(log_decay[h]).  Returns (o, h_final or None).  See include/gla.h.
+
+    q, k [B,H,T,dk], v [B,H,T,dv] with any distances between sequences, heads and tokens (a
+    transposed view of token-major rows is fine); log_decay [H] fp32.  Dense: B sequences of T
+    tokens.  Packed: cu_seqlens [n+1] int32, B = 1, sequence i owns rows cu[i] .. cu[i+1]-1 and
+    none is longer than max_len; rows of no sequence are left as they are in `o`.
+    h0 [slots,H,dk,dv] fp32: start states, sequence i from entry h0_index[i] (int32; default i;
+    negative: zero).  h_final: where the last states go, by h_final_index (negative: nowhere);
+    it may be h0 itself.  Without it, and with want_final, a new [n,H,dk,dv] tensor."""
+    lib = load()
+    B, H, T, dk = q.shape
+    dv = v.shape[-1]
+    dev, dt = q.device, q.dtype
+    if o is None:
+        o = torch.empty(B, H, T, dv, dtype=dt, device=dev)
+    n, max_len, cu, workspace = _decay_setup(q, v, cu_seqlens, max_len, segments, workspace, False)
+    f32, i32 = torch.float32, torch.int32
+    if h_final is None and want_final:
+        if h_final_index is not None:
+            raise ValueError("h_final_index needs h_final")
+        h_final = torch.empty(n, H, dk, dv, dtype=f32, device=dev)
+    slots0, slots1 = (0 if x is None else x.shape[0] for x in (h0, h_final))
+    d = _decay_desc(n, H, T, max_len, dk, dv, dt, slots0, slots1, segments, workspace)
+    r = lib.gla_decay_fwd(ctypes.byref(d), _view(q, "q", dt, (B, H, T, dk), dev), _view(k, "k", dt, (B, H, T, dk), dev),
+                          _view(v, "v", dt, (B, H, T, dv), dev), _dense_ptr(log_decay, "log_decay", f32, (H,), dev), cu,
+                          _dense_ptr(h0, "h0", f32, (slots0, H, dk, dv), dev),
+                          _dense_ptr(h0_index, "h0_index", i32, (n,), dev), _view(o, "o", dt, (B, H, T, dv), dev),
+                          _dense_ptr(h_final, "h_final", f32, (slots1, H, dk, dv), dev),
+                          _dense_ptr(h_final_index, "h_final_index", i32, (n,), dev), _stream_handle(stream))
+    if r != GLA_OK:
+        raise GLAError(r, "gla_decay_fwd")
+    return o, h_final
+
+
+@_on_device
+def gla_decay_bwd(q, k, v, log_decay, do, *, cu_seqlens=None, max_len=None, h0=None, dh_final=None, dq=None, dk=None,
+                  dv=None, dh0=None, want_dh0=True, segments=0, workspace=None, stream=None):
+    """Backward of gla_decay_fwd: (dq, dk, dv, dh0 or None) from do [B,H,T,dv] and dh_final
+    [n,H,dk,dv] (None: zero); h0 [n,H,dk,dv] or None, in order.  The decay is a constant.
+    See include/gla.h."""
+    lib = load()
+    B, H, T, K = q.shape
+    V = v.shape[-1]
+    dev, dt, f32 = q.device, q.dtype, torch.float32
+    n, max_len, cu, workspace = _decay_setup(q, v, cu_seqlens, max_len, segments, workspace, True)
+    dq, dk, dv = (torch.empty_like(like) if t is None else t for t, like in ((dq, q), (dk, k), (dv, v)))
+    if dh0 is None and want_dh0:
+        dh0 = torch.empty(n, H, K, V, dtype=f32, device=dev)
+    d = _decay_desc(n, H, T, max_len, K, V, dt, 0, 0, segments, workspace)
+    sk, sv, ss = (B, H, T, K), (B, H, T, V), (n, H, K, V)
+    r = lib.gla_decay_bwd(ctypes.byref(d), _view(q, "q", dt, sk, dev), _view(k, "k", dt, sk, dev),
+                          _view(v, "v", dt, sv, dev), _dense_ptr(log_decay, "log_decay", f32, (H,), dev), cu,
+                          _dense_ptr(h0, "h0", f32, ss, dev), _view(do, "do", dt, sv, dev),
+                          _dense_ptr(dh_final, "dh_final", f32, ss, dev), _view(dq, "dq", dt, sk, dev),
+                          _view(dk, "dk", dt, sk, dev), _view(dv, "dv", dt, sv, dev),
+                          _dense_ptr(dh0, "dh0", f32, ss, dev), _stream_handle(stream))
+    if r != GLA_OK:
+        raise GLAError(r, "gla_decay_bwd")
+    return dq, dk, dv, dh0
+
+
+@_on_device
+def gla_decay_step(q, k, v, log_decay, state, index=None, *, o=None, workspace=None, stream=None):
+    """One token for each of B running sequences of gla_decay_fwd: state [slots,H,dk,dv] fp32 is
+    updated in place at entry index[b] (int32; default b; negative: a padding row, left out) and
+    o reads it.  q, k [B,H,dk], v [B,H,dv], any distances between rows and heads.  Returns o.
+    workspace: only its status word is used (poll_status).  See include/gla.h."""
+    lib = load()
+    B, H, dk = q.shape
+    dv = v.shape[-1]
+    dev, dt = q.device, q.dtype
+    if o is None:
+        # a padding row's output is not written
+        o = torch.zeros(B, H, dv, dtype=dt, device=dev) if index is not None else torch.empty(B, H, dv, dtype=dt,
+                                                                                             device=dev)
+    d = _decay_desc(B, H, 1, 0, dk, dv, dt, 0, state.shape[0], 0, workspace)
+    r = lib.gla_decay_step(ctypes.byref(d), _view(q, "q", dt, (B, H, dk), dev), _view(k, "k", dt, (B, H, dk), dev),
+                           _view(v, "v", dt, (B, H, dv), dev),
+                           _dense_ptr(log_decay, "log_decay", torch.float32, (H,), dev),
+                           _dense_ptr(state, "state", torch.float32, (state.shape[0], H, dk, dv), dev),
+                           _dense_ptr(index, "index", torch.int32, (B,), dev), _view(o, "o", dt, (B, H, dv), dev),
+                           _stream_handle(stream))
+    if r != GLA_OK:
+        raise GLAError(r, "gla_decay_step")
+    return o
+
+
+def layernorm_workspace_size(rows, d) -> int:
+    """Bytes of workspace for a gla_layernorm_bwd that returns dw or db."""
+    n = load().gla_layernorm_workspace_size(int(rows), int(d))
+    if n == 0:
+        raise GLAError(-2 if rows >= 1 and d >= 1 else -1, "gla_layernorm_workspace_size")
+    return int(n)
+
+
+def _row_view(t, name, like):
+    """(pointer, distance of rows) of [..., d] whose leading dimensions are evenly spaced rows."""
+    _like(t, name, like.dtype, like.shape, like.device)
+    if t.is_contiguous():
+        return t.data_ptr(), t.shape[-1]
+    if t.dim() != 2 or t.stride(1) != 1:
+        raise ValueError(f"{name}: contiguous, or two-dimensional with contiguous rows")
+    return t.data_ptr(), t.stride(0)
+
+
+@_on_device
+def gla_layernorm_fwd(x, w=None, b=None, *, eps=1e-5, y=None, want_stats=True, stream=None):
+    """y = (x - mean) rstd w + b over the last dimension.  x [...,d] (contiguous, or rows of a
+    wider matrix); w, b [d] fp32 or None.  Returns (y, mean, rstd), the statistics [...] in fp32
+    (None without want_stats).  y may be x.  See include/gla.h."""
+    if x.dtype not in DTYPE:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    dev, n = x.device, x.shape[-1]
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    mean = rstd = None
+    if want_stats:
+        mean, rstd = torch.empty((2,) + x.shape[:-1], dtype=torch.float32, device=dev)
+    (px, ldx), (py, ldy) = _row_view(x, "x", x), _row_view(y, "y", x)
+    r = load().gla_layernorm_fwd(DTYPE[x.dtype], x.numel() // max(1, n), n, px, ldx,
+                                 _dense_ptr(w, "w", torch.float32, (n,), dev),
+                                 _dense_ptr(b, "b", torch.float32, (n,), dev), float(eps), py, ldy,
+                                 mean.data_ptr() if want_stats else None, rstd.data_ptr() if want_stats else None,
+                                 _stream_handle(stream))
+    if r != GLA_OK:
+        raise GLAError(r, "gla_layernorm_fwd")
+    return y, mean, rstd
+
+
+@_on_device
+def gla_layernorm_bwd(x, dy, mean, rstd, w=None, *, dx=None, want_dwb=True, workspace=None, stream=None):
+    """Backward of gla_layernorm_fwd: (dx, dw or None, db or None), dw and db [d] fp32 summed
+    over all rows in a fixed order.  mean, rstd from the forward.  dx may be dy."""
+    if x.dtype not in DTYPE:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    dev, n = x.device, x.shape[-1]
+    rows = x.numel() // max(1, n)
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dw = db = None
+    if want_dwb:
+        dw, db = torch.empty(2, n, dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = alloc_workspace(layernorm_workspace_size(rows, n), dev)
+    (px, ldx), (pg, ldg), (po, ldo) = _row_view(x, "x", x), _row_view(dy, "dy", x), _row_view(dx, "dx", x)
+    f32 = torch.float32
+    r = load().gla_layernorm_bwd(DTYPE[x.dtype], rows, n, px, ldx, pg, ldg,
+                                 _dense_ptr(mean, "mean", f32, x.shape[:-1], dev),
+                                 _dense_ptr(rstd, "rstd", f32, x.shape[:-1], dev),
+                                 _dense_ptr(w, "w", f32, (n,), dev), po, ldo, dw.data_ptr() if want_dwb else None,
+                                 db.data_ptr() if want_dwb else None,
+                                 workspace.data_ptr() if workspace is not None else None,
+                                 workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                                 _stream_handle(stream))
+    if r != GLA_OK:
+        raise GLAError(r, "gla_layernorm_bwd")
+    return dx, dw, db
 
 
 def poll_status(workspace: torch.Tensor, stream=None) -> int:

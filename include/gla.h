@@ -57,8 +57,9 @@ extern "C" {
 #define GLA_ERR_WORKSPACE_TOO_SMALL (-4)
 #define GLA_ERR_CUDA (-5)               /* a CUDA runtime / driver call failed          */
 #define GLA_ERR_TIMEOUT (-6)            /* a device-side bounded wait ran out           */
-#define GLA_ERR_GATE_RANGE (-7)         /* a gate too strong for the bf16 rescaling     */
+#define GLA_ERR_GATE_RANGE (-7)         /* a gate too strong for the bf16 rescaling, or a decay above one */
 #define GLA_ERR_NO_DEVICE (-8)          /* no sm_100 device for the bf16 tensor path    */
+#define GLA_ERR_INDEX (-9)              /* a sequence bound or state index out of range, or used twice */
 
 /* Element type of q, k, v, do and of o, dq, dk, dv. */
 #define GLA_DTYPE_BF16 0
@@ -298,6 +299,103 @@ int gla_bwd_state(const gla_desc *desc, const void *q, const void *k, const floa
 int gla_state_scan(const gla_desc *desc, int nseg, int seg, int reverse, const float *gammas, const float *deltas,
                    const float *init, float *out, void *stream);
 
+/* ---- decay attention: heads that forget at a constant rate -----------------------
+ * The recurrence with one decay lambda_h = exp(log_decay[h]) in [0,1] for each head, a
+ * constant of the model ("Gated Linear Attention Transformers with Hardware-Efficient
+ * Training", section 4 and appendix C.2, the data-independent special case):
+ *     S_t = lambda_h S_{t-1} + k_t^T v_t ,     o_t = q_t S_t .
+ * These calls serve batches of sequences of different lengths, packed row after row,
+ * with the carried states in a pool of slots, and take tensors by strides (slices of a
+ * fused projection).  Any decay is exact: every weight lambda^(t-s) is at most one and no
+ * gate is rescaled, so there is no gate range to leave (a learned or token-dependent
+ * decay: gla_fwd / gla_bwd).  The decay has no gradient here.
+ *
+ * gla_view: data and the distance in elements between sequences (sb), heads (sh) and
+ * tokens (st); a token's channels are contiguous.  Every distance is >= 0.
+ * gla_decay_desc:
+ *   dense   (max_len 0, cu_seqlens NULL) B sequences of T tokens each.
+ *   packed  (max_len > 0) cu_seqlens [B+1] int32 on the device, not decreasing: sequence b owns the
+ *           rows cu_seqlens[b] .. cu_seqlens[b+1]-1 of T rows; sb is ignored.  max_len
+ *           (at most T) bounds the longest sequence; a length of zero is allowed.  Rows of
+ *           no sequence are neither read nor written.
+ *   slots0, slots1: entries of the pools h0 and h_final (at least 1 where those are given).
+ *   segments: pieces a long sequence is split into to fill the GPU; 0 = automatic.
+ *   dk <= 256, dv <= 4096, B*H <= 2^20.  bf16 tensors whose data and distances are multiples of 16
+ *   bytes, with dk and dv multiples of 8, run on tcgen05 tensor cores; every other call
+ *   runs on CUDA cores (fp32 arithmetic).
+ *   workspace: 256-byte aligned, gla_decay_workspace_size(desc, for_bwd) bytes.
+ *   Its first 4 bytes are the status word: zero them once; calls only set bits, and
+ *   gla_poll_status reads and clears them (GLA_ERR_TIMEOUT; GLA_ERR_INDEX; GLA_ERR_GATE_RANGE
+ *   for a log_decay that is positive or NaN, taken as 0).  Calls that share a
+ *   workspace must not overlap on the GPU.
+ *
+ * gla_decay_fwd: o and, where h_final is given, the states after each sequence.
+ *   h0 [slots0,H,dk,dv] fp32 or NULL (zero states); sequence b starts from entry
+ *   h0_index[b] (int32 on the device; NULL: entry b; negative: a zero state).
+ *   h_final [slots1,H,dk,dv] or NULL; its entry h_final_index[b] receives sequence b's
+ *   last state (NULL: entry b; negative: not written).  h_final may be h0 (a pool updated
+ *   in place) or must not overlap it.  An index past the pool is reported and treated as negative.  An entry may be written by one sequence of a call only, and a
+ *   pool updated in place read by that sequence only: of two that write one entry the
+ *   first does, one that would read another's entry starts from zero, and both are
+ *   reported (GLA_ERR_INDEX).
+ * gla_decay_bwd: gradients of a loss given do = dL/do and dh_final = dL/dS_T [B,H,dk,dv]
+ *   (NULL: zero): dq, dk, dv and, where given, dh0 [B,H,dk,dv].  h0 [B,H,dk,dv] or NULL.
+ *   The outputs overlap no input.
+ * gla_decay_step: one token for each of B running sequences: the entry index[b] of state
+ *   [slots1,H,dk,dv] (NULL: entry b) is updated in place and o reads it.  q, k, v, o by
+ *   views (st ignored).  A negative index is a padding row: nothing of it is read and its
+ *   row of o is left as it was.  So is the later of two rows with one index, and one past the pool
+ *   (both reported).  Only B, H, dk, dv, dtype, slots1 and the workspace's status word are used; the
+ *   workspace may be NULL (nothing is reported).
+ * A token that is not finite reaches, as in any product of matrices, every output of its
+ * chunk of 128 tokens (64 or 32 on CUDA cores) and all later ones of its sequence, and no other sequence.
+ * All calls validate their arguments before enqueuing anything and run asynchronously on
+ * `stream`, on the device that is current. */
+typedef struct gla_view {
+  void *data;
+  long long sb, sh, st;
+} gla_view;
+
+typedef struct gla_decay_desc {
+  int B, H, T, max_len;
+  int dk, dv;
+  int dtype;            /* GLA_DTYPE_* */
+  int slots0, slots1;
+  int segments;
+  void *workspace;
+  size_t workspace_bytes;
+} gla_decay_desc;
+
+size_t gla_decay_workspace_size(const gla_decay_desc *desc, int for_bwd);
+int gla_decay_fwd(const gla_decay_desc *desc, const gla_view *q, const gla_view *k, const gla_view *v,
+                  const float *log_decay, const int *cu_seqlens, const float *h0, const int *h0_index,
+                  const gla_view *o, float *h_final, const int *h_final_index, void *stream);
+int gla_decay_bwd(const gla_decay_desc *desc, const gla_view *q, const gla_view *k, const gla_view *v,
+                  const float *log_decay, const int *cu_seqlens, const float *h0, const gla_view *do_,
+                  const float *dh_final, const gla_view *dq, const gla_view *dk, const gla_view *dv, float *dh0,
+                  void *stream);
+int gla_decay_step(const gla_decay_desc *desc, const gla_view *q, const gla_view *k, const gla_view *v,
+                   const float *log_decay, float *state, const int *index, const gla_view *o, void *stream);
+
+/* ---- layer norm -------------------------------------------------------------------
+ * The norm in front of a layer: for each of `rows` rows of d values,
+ *     y = (x - mean) rstd w + b ,   rstd = 1 / sqrt(var + eps)   (biased variance).
+ *   x, y, dy, dx: element type dtype, a row's values contiguous, rows ldx, ldy, lddy, lddx
+ *   elements apart (>= d); w, b, dw, db [d] fp32 (w NULL = ones, b NULL = zeros);
+ *   mean, rstd [rows] fp32: written by the forward where given, read by the backward.
+ *   1 <= d <= 16384, 0 < eps < 1, rows >= 1.  y may be x and dx may be dy (in place), or must not overlap.
+ * Statistics are two passes over values held in registers (no E[x^2] - mean^2), in fp32.
+ * gla_layernorm_bwd returns dx and, where given, dw = sum over rows of dy x^ and
+ * db = sum of dy, summed in a fixed order (the same bits every call on one GPU model)
+ * through partial sums in workspace: gla_layernorm_workspace_size(rows, d) bytes,
+ * 256-byte aligned; NULL where neither is asked. */
+size_t gla_layernorm_workspace_size(long long rows, int d);
+int gla_layernorm_fwd(int dtype, long long rows, int d, const void *x, long long ldx, const float *w, const float *b,
+                      float eps, void *y, long long ldy, float *mean, float *rstd, void *stream);
+int gla_layernorm_bwd(int dtype, long long rows, int d, const void *x, long long ldx, const void *dy, long long lddy,
+                      const float *mean, const float *rstd, const float *w, void *dx, long long lddx, float *dw,
+                      float *db, void *workspace, size_t workspace_bytes, void *stream);
+
 /* ---- forward without a workspace ---------------------------------------------
  * No counterpart in the paper: this entry point exists for callers that cannot
  * allocate device memory -- a program whose device memory is all owned by
@@ -334,8 +432,8 @@ int gla_fwd_noalloc(const gla_desc *desc, const void *q, const void *k, const vo
 int gla_poll_status_noalloc(void *stream);
 
 /* Synchronise `stream`, then read and clear the device status word kept in
- * desc->workspace.  Returns GLA_OK, GLA_ERR_TIMEOUT or GLA_ERR_GATE_RANGE (or
- * GLA_ERR_CUDA if the stream itself failed). */
+ * desc->workspace.  Returns GLA_OK, GLA_ERR_TIMEOUT, GLA_ERR_INDEX or
+ * GLA_ERR_GATE_RANGE (or GLA_ERR_CUDA if the stream itself failed). */
 int gla_poll_status(const gla_desc *desc, void *stream);
 
 /* Human-readable text for a return code (static storage). */
