@@ -371,10 +371,6 @@ __global__ void __launch_bounds__(256) k_decay_step(int H, int nseq, int K, int 
 
 }  // namespace
 
-bool decay_tc_takes(const DecayWalk &, int) { return false; }
-int decay_walk_tc(const DecayWalk &, cudaStream_t) { return GLA_ERR_UNSUPPORTED_SHAPE; }
-int decay_chunk_tc() { return 128; }
-
 int decay_chunk_cc(int K) { return K <= 128 ? 64 : 32; }
 
 int decay_walk_cc(const DecayWalk &w, int dtype, cudaStream_t st) {

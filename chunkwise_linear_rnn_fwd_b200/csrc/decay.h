@@ -46,7 +46,6 @@ struct DecayWalk {
 };
 
 // The walk of one call on CUDA cores (decay.cu) and on tensor cores (decay_tc.cu).
-// tc: returns GLA_ERR_UNSUPPORTED_SHAPE, having launched nothing, when it does not take the call.
 int decay_walk_cc(const DecayWalk &w, int dtype, cudaStream_t st);
 bool decay_tc_takes(const DecayWalk &w, int dtype);
 int decay_walk_tc(const DecayWalk &w, cudaStream_t st);

@@ -84,6 +84,18 @@ bool tc::map3_bf16(CUtensorMap *m, const void *base, uint64_t d0, uint64_t d1, u
   return map3(m, base, d0, d1, d2, b0, b1);
 }
 
+bool tc::map4_bf16(CUtensorMap *m, const void *base, const uint64_t *dims, const uint64_t *strides, uint32_t b0,
+                   uint32_t b1) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]}, s[3] = {strides[0], strides[1], strides[2]};
+  cuuint32_t box[4] = {b0, b1, 1, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), d, s, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool tc::map3_store(CUtensorMap *m, const void *base, bool fp32, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0,
                     uint32_t b1) {
   auto fn = encode_fn();

@@ -1,8 +1,15 @@
 // tc_path.h -- bf16 tensor-core (tcgen05 / TMEM / TMA) path, sm_100a.
 #pragma once
+#include <cuda.h>
+
 #include "internal.h"
 
 namespace gla {
+namespace tc {
+// 4-D bf16 tensor map: dims (innermost first), the byte strides of the outer three, box
+// (b0, b1, 1, 1), 128-byte swizzle.
+bool map4_bf16(CUtensorMap *m, const void *base, const uint64_t *dims, const uint64_t *strides, uint32_t b0, uint32_t b1);
+}  // namespace tc
 int tc_check(const Problem &p);
 int selftest_timeout(unsigned *status, unsigned limit_us, cudaStream_t st);
 size_t tc_workspace(const Problem &p, bool bwd);
