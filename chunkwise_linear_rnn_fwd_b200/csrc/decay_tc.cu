@@ -8,27 +8,28 @@
 // factor exceeds one.
 //
 // One CTA per (64 columns of V, segment, sequence and head) and one CTA per SM, 16 warps:
-//   warp 0     TMA loads of X, Y, Z into a ring of chunks
-//   warp 1     issues the products: dS = Y^T Zw (M = channels), X S and P Z (M = tokens,
-//              two accumulators: the row factor f meets the first only), X Y^T
-//   warps 4-7  scores from TMEM, times D, to bf16 in TMEM as the A operand of P Z; later
-//              O from TMEM through a staging tile to global memory
+//   warp 0     TMA loads of X, Y, Z into rings
+//   warp 1     issues the products: X Y^T, X S and P Z (M = tokens, two accumulators: the
+//              row factor f meets X S only), dS = Y^T Zw (M = channels)
+//   warps 4-7  scores from TMEM, times D, to bf16 in TMEM (over the scores, as the A operand
+//              of P Z); later O from TMEM to global memory, a 128-byte row per thread
 //   warps 8-.. one thread per state row (channel): S in fp32 registers, dS from TMEM added,
 //              a bf16 copy to shared memory as the B operand of the next chunk's X S
-//   the rest   w (.) Z as a sum of two bf16 tiles (see below)
+//   the rest   w (.) Z as a sum of three bf16 tiles (see below)
 // The chain from chunk to chunk is dS -> state -> X S, beside it scores -> P -> P Z; the
-// loads run ahead by the ring's depth.
+// loads run ahead by the rings' depth (two tiles of 128 channels of X and of Y).
 //
 // Precision: P and the copy of S that X S reads are rounded to bf16 (2^-8 of each term, the
 // output's own rounding is as large).  The carried state is returned in fp32 and lives on
 // through every later chunk, so its update must not lose that: Y is exact, and w (.) Z is
-// split into a bf16 value and the bf16 rounding of what is left, 2^-16 of each term, at the
-// price of a second product.  lambda^m multiplies the state once a chunk, thousands of
-// times in a long sequence: it is applied as a sum of two fp32 numbers.
+// cut into three bf16 values of eight bits each, which is exact.  The three tiles stand side
+// by side, so that one product of N = 192 columns reads Y once for all.  lambda^m
+// multiplies the state once a chunk, hundreds of times in a long sequence: it is applied as
+// a sum of two fp32 numbers.
 //
-// 64 columns per CTA and not 128: the state, X S and the staging tile shrink, which leaves
-// shared memory for two chunks in flight (one at 256 channels), and a batch of few heads
-// fills twice the SMs.  X Y^T is computed again by every 64 columns; X and Y come from L2.
+// 64 columns per CTA and not 128: the state and X S shrink, which leaves shared memory for
+// two chunks in flight (one at 256 channels), and a batch of few heads fills twice the SMs.
+// X Y^T is computed again by every 64 columns; X and Y come from L2.
 #include "decay.h"
 #include "tc_common.cuh"
 #include "tc_path.h"
@@ -40,36 +41,70 @@ constexpr int kC = 128;   // tokens of a chunk
 constexpr int kBV = 64;   // columns of V per CTA
 constexpr int kThreads = 512;
 constexpr int kTmemCols = 512;
-// TMEM columns: scores fp32, P bf16, the two output accumulators, dS per 128 channels
-constexpr uint32_t kColSc = 0, kColP = 128, kColOa = 192, kColOb = 256, kColDs = 320;
+// TMEM columns: scores fp32 (then P in bf16), the output accumulators, dS (per 128
+// channels 64 columns each for the three parts of Zw; with 256 channels the second and
+// the third part share theirs)
+constexpr uint32_t kColSc = 0, kColOa = 128, kColOb = 192, kColDs = 256;
 
 // KB: 128-channel blocks of the contraction
 template <int KB>
 struct Smem {
-  static constexpr int kStages = KB == 1 ? 2 : 1;
-  static constexpr int kTile = kC * 128 * KB * 2;           // X or Y, SW128 blocks of 64 columns
+  static constexpr int kZStages = KB == 1 ? 2 : 1;
+  static constexpr int kTile = kC * 128 * 2;  // 128 channels of X or Y: two SW128 blocks of 64
   static constexpr int kZTile = kC * kBV * 2;
-  static constexpr int x = 0, y = x + kStages * kTile, z = y + kStages * kTile, zh = z + kStages * kZTile,
-                       zl = zh + kZTile, s = zl + kZTile, o = s + 128 * KB * kBV * 2, w = o + kZTile,
-                       bar = w + 640, bytes = bar + 256;
+  static constexpr int x = 0, y = x + 2 * kTile, z = y + 2 * kTile, zw = z + kZStages * kZTile, s = zw + 3 * kZTile,
+                       t = s + 128 * KB * kBV * 2, bar = t + 672, bytes = bar + 256;
   static_assert(bytes + 1024 <= kMaxDynSmem, "");
 };
+
+__device__ __forceinline__ uint32_t high_halves(uint32_t lo, uint32_t hi) { return __byte_perm(lo, hi, 0x7632); }
+
+// eight bf16 values times f as three bf16 values each, cut (not rounded) so that their sum is the fp32 product
+__device__ __forceinline__ void split3(uint4 u, float f, uint4 &zh, uint4 &zm, uint4 &zl) {
+  const uint32_t a[4] = {u.x, u.y, u.z, u.w};
+  uint32_t h[4], m[4], l[4];
+  const dev::f2 f2v = dev::pk(f, f), neg = dev::pk(-1.f, -1.f);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const dev::f2 p = dev::mul2(dev::bf16pair(a[j]), f2v);
+    float p0, p1;
+    dev::upk(p, p0, p1);
+    h[j] = high_halves(__float_as_uint(p0), __float_as_uint(p1));
+    const dev::f2 q = dev::fma2(dev::bf16pair(h[j]), neg, p);
+    dev::upk(q, p0, p1);
+    m[j] = high_halves(__float_as_uint(p0), __float_as_uint(p1));
+    const dev::f2 r = dev::fma2(dev::bf16pair(m[j]), neg, q);
+    dev::upk(r, p0, p1);
+    l[j] = high_halves(__float_as_uint(p0), __float_as_uint(p1));
+  }
+  zh = make_uint4(h[0], h[1], h[2], h[3]);
+  zm = make_uint4(m[0], m[1], m[2], m[3]);
+  zl = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+__device__ __forceinline__ void st_global_32(void *p, const uint32_t *w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 
 template <int KB, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_decay_tc(const __grid_constant__ DecayWalk w, const __grid_constant__ CUtensorMap tmX,
-               const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmZ,
-               const __grid_constant__ CUtensorMap tmO) {
+               const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmZ) {
   using L = Smem<KB>;
-  constexpr int NS = L::kStages;
+  constexpr int NZ = L::kZStages;
   constexpr int kStateWarps = 4 * KB;
   constexpr int kScale0 = KB == 1 ? 12 : 2, kScaleWarps = KB == 1 ? 4 : 2;
+  constexpr int kDsCols = KB == 1 ? 192 : 128;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  float *W = (float *)(smem + L::w);  // lambda^0 .. lambda^128
+  float *W = (float *)(smem + L::t);  // W[n] = lambda^n, n = 0 .. 128
+  float *Wr = W + 132;                // Wr[e] = lambda^(31-e), e = 0 .. 31
   uint64_t *bars = (uint64_t *)(smem + L::bar);
-  uint64_t *xfull = bars, *xempty = xfull + NS, *yfull = xempty + NS, *yempty = yfull + NS, *zfull = yempty + NS,
-           *zempty = zfull + NS, *scfull = zempty + NS, *pfull = scfull + 1, *ofull = pfull + 1, *oempty = ofull + 1,
+  // slot (i KB + kb) mod 2 of X and Y holds channel block kb of chunk i
+  uint64_t *xfull = bars, *xempty = xfull + 2, *yfull = xempty + 2, *yempty = yfull + 2, *zfull = yempty + 2,
+           *zempty = zfull + 2, *scfull = zempty + 2, *pfull = scfull + 1, *ofull = pfull + 1, *oempty = ofull + 1,
            *dsfull = oempty + 1, *dsempty = dsfull + 1, *sfull = dsempty + 1, *qsdone = sfull + 1, *zready = qsdone + 1,
            *done = zready + 1;
   uint32_t *tslot = (uint32_t *)(done + 1);
@@ -79,19 +114,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int vt = blockIdx.x % tiles, seg = blockIdx.y;
   const long bh = blockIdx.x / tiles;
   const int b = (int)(bh / w.H), h = (int)(bh % w.H), v0 = vt * kBV;
-  const dev::DSeq sq = dev::decay_seq(w, b);
-  const int n = (sq.len + kC - 1) / kC, nseg = max(1, (n + w.L - 1) / w.L);
-  if (seg >= nseg || (!OUT && seg == nseg - 1)) return;  // the whole CTA
-  int i0, i1;
-  dev::decay_slots(w.s0, w.s1, w.alias, w.nseq, b, OUT ? w.status : nullptr, i0, i1);
-  const double rate = dev::decay_rate(w.ld, h, w.status);
-  const int c_begin = seg * w.L, nloc = max(0, min(n, c_begin + w.L) - c_begin);
-  auto chunk_of = [&](int i) { return w.reverse ? n - 1 - (c_begin + i) : c_begin + i; };
-  auto live_of = [&](int i) { return min(kC, sq.len - chunk_of(i) * kC); };
-  const int ksteps = (w.K + 15) / 16, kblocks = (w.K + 63) / 64;
-
   if (tid == 0) {
-    for (int i = 0; i < 6 * NS; ++i) dev::mbar_init(&xfull[i], 1);
+    dev::prefetch_tmap(&tmY);
+    dev::prefetch_tmap(&tmZ);
+    if (OUT) dev::prefetch_tmap(&tmX);
+    for (int i = 0; i < 12; ++i) dev::mbar_init(&xfull[i], 1);
     dev::mbar_init(scfull, 1);
     dev::mbar_init(pfull, 4);
     dev::mbar_init(ofull, 1);
@@ -104,8 +131,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     dev::mbar_init(done, 1);
     dev::fence_mbar_init();
   }
+  const dev::DSeq sq = dev::decay_seq(w, b);
+  const int n = (sq.len + kC - 1) / kC, nseg = max(1, (n + w.L - 1) / w.L);
+  if (seg >= nseg || (!OUT && seg == nseg - 1)) return;  // the whole CTA
+  const int c_begin = seg * w.L, nloc = max(0, min(n, c_begin + w.L) - c_begin);
+  auto chunk_of = [&](int i) { return w.reverse ? n - 1 - (c_begin + i) : c_begin + i; };
+  auto live_of = [&](int i) { return min(kC, sq.len - chunk_of(i) * kC); };
+  const int ksteps = (w.K + 15) / 16, kblocks = (w.K + 63) / 64;
+  // of channel block kb: 16-channel steps, 64-column blocks
+  auto ksteps_of = [&](int kb) { return min(8, ksteps - 8 * kb); };
+  auto kblocks_of = [&](int kb) { return min(2, kblocks - 2 * kb); };
+  auto slot = [&](int i, int kb) { return (i * KB + kb) & 1; };
+  auto phase = [&](int i, int kb) { return (uint32_t)(((i * KB + kb) >> 1) & 1); };
+  auto load_y = [&](int i, int kb) {
+    const int s = slot(i, kb), row = (int)(sq.row0 + (long)chunk_of(i) * kC);
+    dev::mbar_arrive_expect_tx(&yfull[s], (uint32_t)(kblocks_of(kb) * kC * 128));
+    for (int cb = 0; cb < kblocks_of(kb); ++cb)
+      dev::tma_load_4d(smem + L::y + s * L::kTile + cb * kC * 128, &tmY, 128 * kb + cb * 64, row, h, sq.b, &yfull[s]);
+  };
+  auto load_x = [&](int i, int kb) {
+    const int s = slot(i, kb), row = (int)(sq.row0 + (long)chunk_of(i) * kC);
+    dev::mbar_arrive_expect_tx(&xfull[s], (uint32_t)(kblocks_of(kb) * kC * 128));
+    for (int cb = 0; cb < kblocks_of(kb); ++cb)
+      dev::tma_load_4d(smem + L::x + s * L::kTile + cb * kC * 128, &tmX, 128 * kb + cb * 64, row, h, sq.b, &xfull[s]);
+  };
+  auto load_z = [&](int i) {
+    const int s = i % NZ, row = (int)(sq.row0 + (long)chunk_of(i) * kC);
+    dev::mbar_arrive_expect_tx(&zfull[s], (uint32_t)L::kZTile);
+    dev::tma_load_4d(smem + L::z + s * L::kZTile, &tmZ, v0, row, h, sq.b, &zfull[s]);
+  };
+  if (tid == 0 && nloc > 0) {  // the first chunk's loads run beside the set-up
+    for (int kb = 0; kb < KB; ++kb) {
+      if (OUT) load_x(0, kb);
+      load_y(0, kb);
+    }
+    load_z(0);
+  }
   if (warp == 1) dev::tmem_alloc(tslot, kTmemCols);
+  const double rate = dev::decay_rate(w.ld, h, w.status);
   if (tid >= 128 && tid <= 128 + kC) W[tid - 128] = (float)dev::decay_pow(rate, tid - 128);
+  if (tid >= 320 && tid < 352) Wr[tid - 320] = (float)dev::decay_pow(rate, 351 - tid);
+  int i0, i1;
+  dev::decay_slots(w.s0, w.s1, w.alias, w.nseq, b, OUT ? w.status : nullptr, i0, i1);
   dev::tc_fence_before();
   __syncthreads();
   dev::tc_fence_after();
@@ -113,99 +180,128 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ============================ loads ============================
-    if (lane == 0) {
+    if (lane == 0 && nloc > 0) {
       bool ok = true;
-      int xi = 0, yi = 0, zi = 0;  // loads issued
-      for (int i = 0; i < nloc && ok; ++i) {
-        const int s = i % NS;
-        const uint32_t ph = (uint32_t)((i / NS - 1) & 1);
-        const int row = (int)(sq.row0 + (long)chunk_of(i) * kC);
-        if (i >= NS) ok = dev::mbar_wait(&yempty[s], ph, w.status);
-        if (!ok) break;
-        dev::mbar_arrive_expect_tx(&yfull[s], (uint32_t)(kblocks * kC * 128));
-        for (int cb = 0; cb < kblocks; ++cb)
-          dev::tma_load_4d(smem + L::y + s * L::kTile + cb * kC * 128, &tmY, cb * 64, row, h, sq.b, &yfull[s]);
-        ++yi;
-        if (OUT) {
-          if (i >= NS) ok = dev::mbar_wait(&xempty[s], ph, w.status);
-          if (!ok) break;
-          dev::mbar_arrive_expect_tx(&xfull[s], (uint32_t)(kblocks * kC * 128));
-          for (int cb = 0; cb < kblocks; ++cb)
-            dev::tma_load_4d(smem + L::x + s * L::kTile + cb * kC * 128, &tmX, cb * 64, row, h, sq.b, &xfull[s]);
-          ++xi;
+      // the next tile of each kind that has not been issued: (chunk, block)
+      int ni = 1;  // chunks 0 .. ni - 1 are issued
+      int xl = KB, yl = KB, zl = 1;
+      for (; ni < nloc && ok; ++ni) {
+        for (int kb = 0; kb < KB && ok; ++kb) {
+          const int s = slot(ni, kb);
+          if (OUT) {
+            if (ni * KB + kb >= 2) ok = dev::mbar_wait(&xempty[s], phase(ni, kb) ^ 1u, w.status);
+            if (!ok) break;
+            load_x(ni, kb);
+            ++xl;
+          }
         }
-        if (i >= NS) ok = dev::mbar_wait(&zempty[s], ph, w.status);
+        for (int kb = 0; kb < KB && ok; ++kb) {
+          const int s = slot(ni, kb);
+          if (ni * KB + kb >= 2) ok = dev::mbar_wait(&yempty[s], phase(ni, kb) ^ 1u, w.status);
+          if (!ok) break;
+          load_y(ni, kb);
+          ++yl;
+        }
+        if (ok && ni >= NZ) ok = dev::mbar_wait(&zempty[ni % NZ], (uint32_t)((ni / NZ - 1) & 1), w.status);
         if (!ok) break;
-        dev::mbar_arrive_expect_tx(&zfull[s], (uint32_t)L::kZTile);
-        dev::tma_load_4d(smem + L::z + s * L::kZTile, &tmZ, v0, row, h, sq.b, &zfull[s]);
-        ++zi;
+        load_z(ni);
+        ++zl;
       }
       // every load issued lands before the CTA ends, also where a wait ran out
-      for (int j = max(0, yi - NS); j < yi; ++j) (void)dev::mbar_wait(&yfull[j % NS], (uint32_t)((j / NS) & 1), w.status);
-      for (int j = max(0, xi - NS); j < xi; ++j) (void)dev::mbar_wait(&xfull[j % NS], (uint32_t)((j / NS) & 1), w.status);
-      for (int j = max(0, zi - NS); j < zi; ++j) (void)dev::mbar_wait(&zfull[j % NS], (uint32_t)((j / NS) & 1), w.status);
+      for (int j = max(0, yl - 2); j < yl; ++j) (void)dev::mbar_wait(&yfull[j & 1], (uint32_t)((j >> 1) & 1), w.status);
+      if (OUT)
+        for (int j = max(0, xl - 2); j < xl; ++j) (void)dev::mbar_wait(&xfull[j & 1], (uint32_t)((j >> 1) & 1), w.status);
+      for (int j = max(0, zl - NZ); j < zl; ++j) (void)dev::mbar_wait(&zfull[j % NZ], (uint32_t)((j / NZ) & 1), w.status);
     }
   } else if (warp == 1) {
     // ============================ products ============================
     if (lane == 0) {
       constexpr uint32_t id_sc = dev::idesc_bf16(kC, kC, false, false);   // X, Y: K-major
       constexpr uint32_t id_o = dev::idesc_bf16(kC, kBV, false, true);    // X or P (TMEM); S or Z: MN-major
-      constexpr uint32_t id_ds = dev::idesc_bf16(128, kBV, true, true);   // Y, Zw: MN-major
-      const uint32_t sS = dev::smem_u32(smem + L::s), sZh = dev::smem_u32(smem + L::zh), sZl = dev::smem_u32(smem + L::zl);
+      constexpr uint32_t id_ds = dev::idesc_bf16(128, kDsCols, true, true);  // Y, Zw: MN-major
+      constexpr uint32_t id_dl = dev::idesc_bf16(128, kBV, true, true);
+      const uint32_t sX = dev::smem_u32(smem + L::x), sY = dev::smem_u32(smem + L::y), sZ = dev::smem_u32(smem + L::z),
+                     sS = dev::smem_u32(smem + L::s), sZw = dev::smem_u32(smem + L::zw);
       bool ok = true;
+      // X Y^T of chunk i
       auto scores = [&](int i) {
-        const int s = i % NS;
-        const uint32_t ph = (uint32_t)((i / NS) & 1);
-        ok = dev::mbar_wait(&xfull[s], ph, w.status) && dev::mbar_wait(&yfull[s], ph, w.status);
-        if (!ok) return;
-        dev::tc_fence_after();
-        const uint32_t sX = dev::smem_u32(smem + L::x + s * L::kTile), sY = dev::smem_u32(smem + L::y + s * L::kTile);
-        for (int kk = 0; kk < ksteps; ++kk)
-          dev::umma_bf16(tmem + kColSc, dev::desc_kmajor(sX, kC, 0, kk * 16), dev::desc_kmajor(sY, kC, 0, kk * 16), id_sc,
-                         kk > 0 ? 1u : 0u);
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          const int s = slot(i, kb);
+          ok = ok && dev::mbar_wait(&xfull[s], phase(i, kb), w.status) && dev::mbar_wait(&yfull[s], phase(i, kb), w.status);
+          if (!ok) return;
+          dev::tc_fence_after();
+          const int ks = ksteps_of(kb);
+          for (int kk = 0; kk < ks; ++kk)
+            dev::umma_bf16(tmem + kColSc, dev::desc_kmajor(sX + s * L::kTile, kC, 0, kk * 16),
+                           dev::desc_kmajor(sY + s * L::kTile, kC, 0, kk * 16), id_sc, kb + kk > 0 ? 1u : 0u);
+          if (KB == 2) dev::umma_commit(&xempty[s]);  // X S came first
+        }
         dev::umma_commit(scfull);
       };
-      if (OUT && nloc > 0) scores(0);
+      // X S of chunk i
+      auto inter = [&](int i) {
+        ok = ok && dev::mbar_wait(sfull, (uint32_t)(i & 1), w.status);
+        if (ok && i > 0) ok = dev::mbar_wait(oempty, (uint32_t)((i & 1) ^ 1), w.status);
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          const int s = slot(i, kb);
+          ok = ok && dev::mbar_wait(&xfull[s], phase(i, kb), w.status);
+          if (!ok) return;
+          dev::tc_fence_after();
+          const int ks = ksteps_of(kb);
+          for (int kk = 0; kk < ks; ++kk)
+            dev::umma_bf16(tmem + kColOb, dev::desc_kmajor(sX + s * L::kTile, kC, 0, kk * 16),
+                           dev::desc_mnmajor(sS, 128 * KB, 128 * kb + kk * 16, 0), id_o, kb + kk > 0 ? 1u : 0u);
+          if (KB == 1) dev::umma_commit(&xempty[s]);  // X Y^T came first
+        }
+        dev::umma_commit(qsdone);
+      };
       for (int i = 0; i < nloc && ok; ++i) {
-        const int s = i % NS;
-        const uint32_t ph = (uint32_t)((i / NS) & 1), par = (uint32_t)(i & 1);
+        const uint32_t par = (uint32_t)(i & 1);
         const int tsteps = (live_of(i) + 15) / 16;  // 16-token steps that hold a live token
-        const uint32_t sX = dev::smem_u32(smem + L::x + s * L::kTile), sY = dev::smem_u32(smem + L::y + s * L::kTile),
-                       sZ = dev::smem_u32(smem + L::z + s * L::kZTile);
-        ok = dev::mbar_wait(&yfull[s], ph, w.status) && dev::mbar_wait(&zfull[s], ph, w.status) &&
+        // With 128 channels X Y^T goes first, so that P is ready by the time dS is done; with
+        // 256 X S does, while the next Y, which has no second buffer, arrives.
+        if (OUT) {
+          if (KB == 1) {
+            scores(i);
+            inter(i);
+          } else {
+            inter(i);
+            scores(i);
+          }
+        }
+        ok = ok && dev::mbar_wait(&zfull[i % NZ], (uint32_t)((i / NZ) & 1), w.status) &&
              dev::mbar_wait(zready, par, w.status);
         if (ok && i > 0) ok = dev::mbar_wait(dsempty, par ^ 1u, w.status);
         if (!ok) break;
-        dev::tc_fence_after();
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-          for (int kk = 0; kk < tsteps; ++kk) {
-            const uint64_t dy = dev::desc_mnmajor(sY, kC, kk * 16, 128 * kb);
-            dev::umma_bf16(tmem + kColDs + kb * kBV, dy, dev::desc_mnmajor(sZh, kC, kk * 16, 0), id_ds, kk > 0 ? 1u : 0u);
-            dev::umma_bf16(tmem + kColDs + kb * kBV, dy, dev::desc_mnmajor(sZl, kC, kk * 16, 0), id_ds, 1u);
-          }
-        dev::umma_commit(dsfull);
-        dev::umma_commit(&yempty[s]);
-        if (OUT) {
-          ok = dev::mbar_wait(sfull, par, w.status);
-          if (ok && i > 0) ok = dev::mbar_wait(oempty, par ^ 1u, w.status);
+        for (int kb = 0; kb < KB; ++kb) {
+          const int s = slot(i, kb);
+          ok = ok && dev::mbar_wait(&yfull[s], phase(i, kb), w.status);
           if (!ok) break;
           dev::tc_fence_after();
-          for (int kk = 0; kk < ksteps; ++kk)
-            dev::umma_bf16(tmem + kColOb, dev::desc_kmajor(sX, kC, 0, kk * 16), dev::desc_mnmajor(sS, 128 * KB, kk * 16, 0),
-                           id_o, kk > 0 ? 1u : 0u);
-          dev::umma_commit(qsdone);
-          dev::umma_commit(&xempty[s]);
+          for (int kk = 0; kk < tsteps; ++kk) {
+            const uint64_t dy = dev::desc_mnmajor(sY + s * L::kTile, kC, kk * 16, 0);
+            dev::umma_bf16(tmem + kColDs + kb * 128, dy, dev::desc_mnmajor(sZw, kC, kk * 16, 0), id_ds, kk > 0 ? 1u : 0u);
+            if (KB == 2)
+              dev::umma_bf16(tmem + kColDs + kb * 128 + kBV, dy, dev::desc_mnmajor(sZw + 2 * L::kZTile, kC, kk * 16, 0),
+                             id_dl, 1u);
+          }
+          dev::umma_commit(&yempty[s]);
+        }
+        if (!ok) break;
+        dev::umma_commit(dsfull);
+        if (OUT) {
           ok = dev::mbar_wait(pfull, par, w.status);
           if (!ok) break;
           dev::tc_fence_after();
           for (int kk = 0; kk < tsteps; ++kk)
-            dev::umma_bf16_ts(tmem + kColOa, tmem + kColP + kk * 8, dev::desc_mnmajor(sZ, kC, kk * 16, 0), id_o,
-                              kk > 0 ? 1u : 0u);
+            dev::umma_bf16_ts(tmem + kColOa, tmem + kColSc + kk * 8,
+                              dev::desc_mnmajor(sZ + (i % NZ) * L::kZTile, kC, kk * 16, 0), id_o, kk > 0 ? 1u : 0u);
           dev::umma_commit(ofull);
         }
-        dev::umma_commit(&zempty[s]);
-        if (OUT && i + 1 < nloc) scores(i + 1);
+        dev::umma_commit(&zempty[i % NZ]);
       }
       dev::umma_commit(done);  // all products have completed before TMEM is released
       (void)dev::mbar_wait(done, 0, w.status);
@@ -213,44 +309,56 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kScale0 && warp < kScale0 + kScaleWarps) {
     // ============================ w (.) Z ============================
     const int t0 = tid - 32 * kScale0;
+    constexpr int kStep = 32 * kScaleWarps, kIter = kC * 8 / kStep;  // 16-byte units per pass, passes
     bool ok = true;
-    for (int i = 0; i < nloc; ++i) {
-      const int s = i % NS;
-      const uint32_t ph = (uint32_t)((i / NS) & 1);
-      const int m = live_of(i), m16 = (m + 15) & ~15;
-      if (ok) ok = dev::mbar_wait(&zfull[s], ph, w.status);
-      if (ok && m < m16) ok = dev::mbar_wait(&yfull[s], ph, w.status);
-      if (ok && i > 0) ok = dev::mbar_wait(dsfull, (uint32_t)((i - 1) & 1), w.status);
-      if (ok) {
-        uint8_t *zt = smem + L::z + s * L::kZTile;
-        // a row is eight 16-byte units; their place in the swizzled row does not matter here
-#pragma unroll 4
-        for (int e = t0; e < m16 * 8; e += 32 * kScaleWarps) {
-          const int r = e >> 3;
-          uint4 u = *reinterpret_cast<const uint4 *>(zt + e * 16), hi, lo;
-          // rows behind the sequence hold anything: zero times it must not be NaN
-          if (r >= m) {
-            u = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4 *>(zt + e * 16) = u;
-          }
-          const float f = W[r < m ? (w.reverse ? r + 1 : m - 1 - r) : 0];
-          const uint32_t a[4] = {u.x, u.y, u.z, u.w};
-          uint32_t ah[4], al[4];
+    float wf[kIter];  // the weights of a whole chunk: this thread's rows are t0 / 8 + (kStep / 8) j
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float p = __uint_as_float(a[j] << 16) * f, q = __uint_as_float(a[j] & 0xffff0000u) * f;
-            ah[j] = dev::pack_bf16(p, q);
-            al[j] = dev::pack_bf16(p - __uint_as_float(ah[j] << 16), q - __uint_as_float(ah[j] & 0xffff0000u));
-          }
-          hi = make_uint4(ah[0], ah[1], ah[2], ah[3]);
-          lo = make_uint4(al[0], al[1], al[2], al[3]);
-          *reinterpret_cast<uint4 *>(smem + L::zh + e * 16) = hi;
-          *reinterpret_cast<uint4 *>(smem + L::zl + e * 16) = lo;
+    for (int j = 0; j < kIter; ++j) {
+      const int r = (t0 + j * kStep) >> 3;
+      wf[j] = W[w.reverse ? r + 1 : kC - 1 - r];
+    }
+    for (int i = 0; i < nloc; ++i) {
+      const int s = i % NZ;
+      const int m = live_of(i);
+      if (ok) ok = dev::mbar_wait(&zfull[s], (uint32_t)((i / NZ) & 1), w.status);
+      if (ok && i > 0) ok = dev::mbar_wait(dsfull, (uint32_t)((i - 1) & 1), w.status);
+      uint8_t *zt = smem + L::z + s * L::kZTile, *zw = smem + L::zw;
+      // a row is eight 16-byte units; their place in the swizzled row does not matter here
+      if (ok && m == kC) {
+#pragma unroll
+        for (int j = 0; j < kIter; ++j) {
+          const int e = 16 * (t0 + j * kStep);
+          uint4 zh, zm, zl;
+          split3(*reinterpret_cast<const uint4 *>(zt + e), wf[j], zh, zm, zl);
+          *reinterpret_cast<uint4 *>(zw + e) = zh;
+          *reinterpret_cast<uint4 *>(zw + L::kZTile + e) = zm;
+          *reinterpret_cast<uint4 *>(zw + 2 * L::kZTile + e) = zl;
         }
-        uint8_t *yt = smem + L::y + s * L::kTile;
+      } else if (ok) {
+        // rows behind the sequence hold anything, and zero times it must not be NaN: those
+        // that the products read are cleared
+        const int m16 = (m + 15) & ~15;
+        for (int u = t0; u < m16 * 8; u += kStep) {
+          const int r = u >> 3, e = 16 * u;
+          uint4 zh, zm, zl, a = *reinterpret_cast<const uint4 *>(zt + e);
+          if (r >= m) {
+            a = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(zt + e) = a;
+          }
+          split3(a, W[r < m ? (w.reverse ? r + 1 : m - 1 - r) : 0], zh, zm, zl);
+          *reinterpret_cast<uint4 *>(zw + e) = zh;
+          *reinterpret_cast<uint4 *>(zw + L::kZTile + e) = zm;
+          *reinterpret_cast<uint4 *>(zw + 2 * L::kZTile + e) = zl;
+        }
         const int dead = (m16 - m) * 8;
-        for (int e = t0; e < dead * kblocks; e += 32 * kScaleWarps)
-          *reinterpret_cast<uint4 *>(yt + (e / dead) * kC * 128 + m * 128 + (e % dead) * 16) = make_uint4(0, 0, 0, 0);
+        for (int kb = 0; kb < KB; ++kb) {
+          const int sy = slot(i, kb);
+          if (ok) ok = dev::mbar_wait(&yfull[sy], phase(i, kb), w.status);
+          if (!ok) break;
+          for (int u = t0; u < dead * kblocks_of(kb); u += kStep)
+            *reinterpret_cast<uint4 *>(smem + L::y + sy * L::kTile + (u / dead) * kC * 128 + m * 128 + (u % dead) * 16) =
+                make_uint4(0, 0, 0, 0);
+        }
       }
       dev::fence_proxy_async_smem();
       __syncwarp();
@@ -261,8 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (OUT) {
       const int q4 = warp & 3, t = 32 * q4 + lane;
       const uint32_t lane_base = tmem + ((uint32_t)(32 * q4) << 16);
-      uint8_t *stage = smem + L::o;
       const long rows = w.packed ? w.T : (long)w.nseq * w.T;
+      const bool wide = (((uintptr_t)w.o.p | (uintptr_t)(2 * w.o.st) | (uintptr_t)(2 * w.o.sh) | (uintptr_t)(2 * w.o.sb)) & 31u) == 0;
+      const int nv = min(kBV, w.V - v0);  // a multiple of 8
       bool ok = true;
       for (int i = 0; i < nloc; ++i) {
         const uint32_t par = (uint32_t)(i & 1);
@@ -270,7 +379,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long row0 = sq.row0 + (long)chunk_of(i) * kC;
         if (ok) ok = dev::mbar_wait(scfull, par, w.status);
         dev::tc_fence_after();
-        // 32 columns (tokens j) at a time; blocks on the far side of the diagonal are zero
+        // 32 columns (tokens j) at a time.  P's columns 16 jb .. lie over scores that this
+        // warp has read.  Blocks on the far side of the diagonal are zero.  On the near side
+        // the weight is one factor per thread times one per column: forward
+        // lambda^(t-j) = lambda^(t - 32 jb - 31) lambda^(31 - e), j = 32 jb + e, reverse
+        // lambda^(j-t) = lambda^(32 jb - t) lambda^e.
 #pragma unroll 1
         for (int jb = 0; jb < 4; ++jb) {
           uint32_t p[16];
@@ -280,16 +393,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             float sc[32];
             dev::tmem_ld32(lane_base + kColSc + 32 * jb, sc);
+            const float *col = w.reverse ? W : Wr;
+            const float a = W[jb == q4 ? 0 : (w.reverse ? 32 * jb - t : t - 32 * jb - 31)];
+            float f[32];
+            if (jb == q4) {
+              // the diagonal block: |lane - e| steps apart; what lies beyond it is not
+              // multiplied by zero but replaced, it may be anything
+#pragma unroll
+              for (int e = 0; e < 32; ++e) f[e] = W[abs(lane - e)];
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float4 c = *reinterpret_cast<const float4 *>(col + e);
+                f[e] = a * c.x, f[e + 1] = a * c.y, f[e + 2] = a * c.z, f[e + 3] = a * c.w;
+              }
+            }
             dev::tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int j = 32 * jb + e, g = w.reverse ? j - t : t - j;
-              sc[e] = g >= 0 && j < m ? sc[e] * W[g & 127] : 0.f;
+            for (int e = 0; e < 32; ++e) sc[e] *= f[e];
+            if (jb == q4) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) sc[e] = (w.reverse ? e >= lane : e <= lane) ? sc[e] : 0.f;
+            }
+            if (w.reverse && m < kC) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) sc[e] = 32 * jb + e < m ? sc[e] : 0.f;
             }
 #pragma unroll
             for (int e = 0; e < 16; ++e) p[e] = dev::pack_bf16(sc[2 * e], sc[2 * e + 1]);
           }
-          dev::tmem_st16u(lane_base + kColP + 16 * jb, p);
+          dev::tmem_st16u(lane_base + kColSc + 16 * jb, p);
         }
         dev::tmem_wait_st();
         dev::tc_fence_before();
@@ -299,8 +432,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) ok = dev::mbar_wait(ofull, par, w.status);
         dev::tc_fence_after();
         const float f = W[t < m ? (w.reverse ? m - 1 - t : t + 1) : 0];
-        if (tid == 128) dev::tma_store_wait_read();  // the store of the chunk before has read the tile
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        __nv_bfloat16 *o = (__nv_bfloat16 *)w.o.p + sq.b * w.o.sb + h * w.o.sh + (row0 + t) * w.o.st + v0;
+        const bool live = t < m && ok;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           float a[32], c[32];
@@ -314,12 +447,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int e = 0; e < 32; ++e) a[e] = fmaf(f, c[e], a[e]);
-          if ((w.acc_in || w.acc_out) && t < m && ok) {
+          if (!live) continue;
+          if (w.acc_in || w.acc_out) {
             const long row = w.packed ? row0 + t : (long)b * w.T + row0 + t;
             float *part = w.acc + ((long)h * rows + row) * w.V + v0 + 32 * hf;
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              if (v0 + 32 * hf + e < w.V) {
+              if (32 * hf + e < nv) {
                 float4 x = make_float4(a[e], a[e + 1], a[e + 2], a[e + 3]);
                 if (w.acc_in) {
                   const float4 y = *reinterpret_cast<const float4 *>(part + e);
@@ -328,34 +462,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (w.acc_out) *reinterpret_cast<float4 *>(part + e) = x;
               }
+            if (w.acc_out) continue;
           }
-          const uint32_t so = dev::smem_u32(stage) + (uint32_t)t * 128u;
+          uint32_t r[16];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            dev::st_shared_v4(so + (uint32_t)(((4 * hf + j) ^ (t & 7)) << 4), dev::pack_bf16(a[8 * j], a[8 * j + 1]),
-                              dev::pack_bf16(a[8 * j + 2], a[8 * j + 3]), dev::pack_bf16(a[8 * j + 4], a[8 * j + 5]),
-                              dev::pack_bf16(a[8 * j + 6], a[8 * j + 7]));
-        }
-        dev::fence_proxy_async_smem();
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (ok && !w.acc_out) {
-          if (m == kC) {
-            if (tid == 128) {
-              dev::tma_store_4d(&tmO, stage, v0, (int)row0, h, sq.b);
-              dev::tma_store_commit();
-            }
-          } else {  // rows behind the sequence are not this one's to write
-            __nv_bfloat16 *o = (__nv_bfloat16 *)w.o.p + sq.b * w.o.sb + h * w.o.sh + row0 * w.o.st + v0;
-            for (int e = tid - 128; e < m * 8; e += 128) {
-              const int r = e >> 3, j = e & 7;
-              if (v0 + 8 * j < w.V)
-                *reinterpret_cast<uint4 *>(o + r * w.o.st + 8 * j) =
-                    *reinterpret_cast<const uint4 *>(stage + r * 128 + ((j ^ (r & 7)) << 4));
-            }
+          for (int e = 0; e < 16; ++e) r[e] = dev::pack_bf16(a[2 * e], a[2 * e + 1]);
+          if (wide && nv == kBV) {
+            st_global_32(o + 32 * hf, r);
+            st_global_32(o + 32 * hf + 16, r + 8);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (32 * hf + 8 * j < nv)
+                *reinterpret_cast<uint4 *>(o + 32 * hf + 8 * j) =
+                    make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
           }
         }
       }
-      if (tid == 128) dev::tma_store_wait_all();
     }
   } else if (warp >= 8 && warp < 8 + kStateWarps) {
     // ============================ state ============================
@@ -431,18 +554,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ok) ok = dev::mbar_wait(dsfull, (uint32_t)(i & 1), w.status);
       dev::tc_fence_after();
+      // the parts of dS 16 columns at a time, the small ones added first
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        float d[32];
-        dev::tmem_ld32(lane_base + kColDs + kb * kBV + 32 * hf, d);
+      for (int g = 0; g < 4; ++g) {
+        float d0[16], d1[16], d2[16];
+        const uint32_t c = lane_base + kColDs + kb * 128 + 16 * g;
+        dev::tmem_ld16(c, d0);
+        dev::tmem_ld16(c + kBV, d1);
+        if (KB == 1) dev::tmem_ld16(c + 2 * kBV, d2);
         dev::tmem_wait_ld();
-        if (hf == 1) {
+        if (g == 3) {
           dev::tc_fence_before();
           __syncwarp();
           if (lane == 0) dev::mbar_arrive(dsempty);
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) S[32 * hf + e] = fmaf(S[32 * hf + e], dh, fmaf(S[32 * hf + e], dl, d[e]));
+        for (int e = 0; e < 16; ++e) {
+          const float lo = KB == 1 ? d2[e] + d1[e] : d1[e];
+          S[16 * g + e] = fmaf(S[16 * g + e], dh, fmaf(S[16 * g + e], dl, lo) + d0[e]);
+        }
       }
       if (OUT && i + 1 < nloc) {
         if (ok) ok = dev::mbar_wait(qsdone, (uint32_t)(i & 1), w.status);
@@ -495,9 +625,8 @@ bool make_map(CUtensorMap *m, const DView &v, const DecayWalk &w, int channels) 
 
 template <int KB>
 int launch(const DecayWalk &w, cudaStream_t st) {
-  CUtensorMap mx, my, mz, mo;
-  if (!make_map(&mx, w.x, w, w.K) || !make_map(&my, w.y, w, w.K) || !make_map(&mz, w.z, w, w.V) ||
-      !make_map(&mo, w.o, w, w.V))
+  CUtensorMap mx, my, mz;
+  if (!make_map(&mx, w.x, w, w.K) || !make_map(&my, w.y, w, w.K) || !make_map(&mz, w.z, w, w.V))
     return GLA_ERR_CUDA;
   const int smem = Smem<KB>::bytes + 1024;
   if (cudaFuncSetAttribute(k_decay_tc<KB, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
@@ -505,8 +634,8 @@ int launch(const DecayWalk &w, cudaStream_t st) {
     return GLA_ERR_CUDA;
   const unsigned gx = (unsigned)((long)w.nseq * w.H * ((w.V + kBV - 1) / kBV));
   if (w.P > 1)
-    GLA_LAUNCH(K_DECAY_STATES, st, (k_decay_tc<KB, false><<<dim3(gx, w.P - 1), kThreads, smem, st>>>(w, mx, my, mz, mo)));
-  GLA_LAUNCH(K_DECAY_WALK, st, (k_decay_tc<KB, true><<<dim3(gx, w.P), kThreads, smem, st>>>(w, mx, my, mz, mo)));
+    GLA_LAUNCH(K_DECAY_STATES, st, (k_decay_tc<KB, false><<<dim3(gx, w.P - 1), kThreads, smem, st>>>(w, mx, my, mz)));
+  GLA_LAUNCH(K_DECAY_WALK, st, (k_decay_tc<KB, true><<<dim3(gx, w.P), kThreads, smem, st>>>(w, mx, my, mz)));
   return GLA_OK;
 }
 
