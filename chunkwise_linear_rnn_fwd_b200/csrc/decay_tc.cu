@@ -16,14 +16,16 @@
 //   warps 8-.. one thread per state row (channel): S in fp32 registers, dS from TMEM added,
 //              a bf16 copy to shared memory as the B operand of the next chunk's X S
 //   the rest   w (.) Z as a sum of three bf16 tiles (see below)
+// The products are issued by one thread of a converged warp from descriptors that differ by
+// constants: formed anew in a loop they took 180 cycles each, longer than the products.
 // The chain from chunk to chunk is dS -> state -> X S, beside it scores -> P -> P Z; the
 // loads run ahead by the rings' depth (two tiles of 128 channels of X and of Y).
 //
 // Precision: P and the copy of S that X S reads are rounded to bf16 (2^-8 of each term, the
 // output's own rounding is as large).  The carried state is returned in fp32 and lives on
 // through every later chunk, so its update must not lose that: Y is exact, and w (.) Z is
-// cut into three bf16 values of eight bits each, which is exact.  The three tiles stand side
-// by side, so that one product of N = 192 columns reads Y once for all.  lambda^m
+// cut into three bf16 values of eight bits each, which is exact.  Two of the three tiles
+// stand side by side, so that one product of N = 128 columns reads Y for both.  lambda^m
 // multiplies the state once a chunk, hundreds of times in a long sequence: it is applied as
 // a sum of two fp32 numbers.
 //
@@ -42,9 +44,16 @@ constexpr int kBV = 64;   // columns of V per CTA
 constexpr int kThreads = 512;
 constexpr int kTmemCols = 512;
 // TMEM columns: scores fp32 (then P in bf16), the output accumulators, dS (per 128
-// channels 64 columns each for the three parts of Zw; with 256 channels the second and
-// the third part share theirs)
+// channels 64 columns for the first part of Zw and 64 for the two others)
 constexpr uint32_t kColSc = 0, kColOa = 128, kColOb = 192, kColDs = 256;
+
+// Registers a thread, per warpgroup.  Launched with 128; the groups that wait and issue give
+// some to those that hold rows of scores and of the state.
+template <int KB>
+struct Regs {
+  static constexpr int roles = KB == 1 ? 80 : 96, rows = 160, state = KB == 1 ? 168 : 128, scale = 96;
+  static_assert(roles + rows + (KB == 1 ? state + scale : 2 * state) <= 4 * 128, "more than the launch allocates");
+};
 
 // KB: 128-channel blocks of the contraction
 template <int KB>
@@ -53,7 +62,7 @@ struct Smem {
   static constexpr int kTile = kC * 128 * 2;  // 128 channels of X or Y: two SW128 blocks of 64
   static constexpr int kZTile = kC * kBV * 2;
   static constexpr int x = 0, y = x + 2 * kTile, z = y + 2 * kTile, zw = z + kZStages * kZTile, s = zw + 3 * kZTile,
-                       t = s + 128 * KB * kBV * 2, bar = t + 672, bytes = bar + 256;
+                       t = s + 128 * KB * kBV * 2, bar = t + 928, bytes = bar + 256;
   static_assert(bytes + 1024 <= kMaxDynSmem, "");
 };
 
@@ -88,7 +97,7 @@ __device__ __forceinline__ void st_global_32(void *p, const uint32_t *w) {
                : "memory");
 }
 
-template <int KB, bool OUT>
+template <int KB, bool OUT, bool REV>
 __global__ void __launch_bounds__(kThreads, 1)
     k_decay_tc(const __grid_constant__ DecayWalk w, const __grid_constant__ CUtensorMap tmX,
                const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmZ) {
@@ -96,11 +105,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int NZ = L::kZStages;
   constexpr int kStateWarps = 4 * KB;
   constexpr int kScale0 = KB == 1 ? 12 : 2, kScaleWarps = KB == 1 ? 4 : 2;
-  constexpr int kDsCols = KB == 1 ? 192 : 128;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   float *W = (float *)(smem + L::t);  // W[n] = lambda^n, n = 0 .. 128
   float *Wr = W + 132;                // Wr[e] = lambda^(31-e), e = 0 .. 31
+  float *Wd = Wr + 32;                // Wd[31+n] = lambda^n, n = 0 .. 31; zero below
   uint64_t *bars = (uint64_t *)(smem + L::bar);
   // slot (i KB + kb) mod 2 of X and Y holds channel block kb of chunk i
   uint64_t *xfull = bars, *xempty = xfull + 2, *yfull = xempty + 2, *yempty = yfull + 2, *zfull = yempty + 2,
@@ -135,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n = (sq.len + kC - 1) / kC, nseg = max(1, (n + w.L - 1) / w.L);
   if (seg >= nseg || (!OUT && seg == nseg - 1)) return;  // the whole CTA
   const int c_begin = seg * w.L, nloc = max(0, min(n, c_begin + w.L) - c_begin);
-  auto chunk_of = [&](int i) { return w.reverse ? n - 1 - (c_begin + i) : c_begin + i; };
+  auto chunk_of = [&](int i) { return REV ? n - 1 - (c_begin + i) : c_begin + i; };
   auto live_of = [&](int i) { return min(kC, sq.len - chunk_of(i) * kC); };
   const int ksteps = (w.K + 15) / 16, kblocks = (w.K + 63) / 64;
   // of channel block kb: 16-channel steps, 64-column blocks
@@ -170,15 +179,82 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) dev::tmem_alloc(tslot, kTmemCols);
   const double rate = dev::decay_rate(w.ld, h, w.status);
   if (tid >= 128 && tid <= 128 + kC) W[tid - 128] = (float)dev::decay_pow(rate, tid - 128);
-  if (tid >= 320 && tid < 352) Wr[tid - 320] = (float)dev::decay_pow(rate, 351 - tid);
+  if (tid >= 320 && tid < 352) {
+    Wr[tid - 320] = (float)dev::decay_pow(rate, 351 - tid);
+    Wd[tid - 289] = (float)dev::decay_pow(rate, tid - 320);
+    if (tid < 351) Wd[tid - 320] = 0.f;
+  }
   int i0, i1;
   dev::decay_slots(w.s0, w.s1, w.alias, w.nseq, b, OUT ? w.status : nullptr, i0, i1);
   dev::tc_fence_before();
   __syncthreads();
   dev::tc_fence_after();
   const uint32_t tmem = *tslot;
+  using R = Regs<KB>;
 
-  if (warp == 0) {
+  // ============================ w (.) Z ============================
+  auto scale_z = [&]() {
+    const int t0 = tid - 32 * kScale0;
+    constexpr int kStep = 32 * kScaleWarps, kIter = kC * 8 / kStep;  // 16-byte units per pass, passes
+    bool ok = true;
+    float wf[kIter];  // the weights of a whole chunk: this thread's rows are t0 / 8 + (kStep / 8) j
+#pragma unroll
+    for (int j = 0; j < kIter; ++j) {
+      const int r = (t0 + j * kStep) >> 3;
+      wf[j] = W[REV ? r + 1 : kC - 1 - r];
+    }
+    for (int i = 0; i < nloc; ++i) {
+      const int s = i % NZ;
+      const int m = live_of(i);
+      if (ok) ok = dev::mbar_wait(&zfull[s], (uint32_t)((i / NZ) & 1), w.status);
+      if (ok && i > 0) ok = dev::mbar_wait(dsfull, (uint32_t)((i - 1) & 1), w.status);
+      uint8_t *zt = smem + L::z + s * L::kZTile, *zw = smem + L::zw;
+      // a row is eight 16-byte units; their place in the swizzled row does not matter here
+      if (ok && m == kC) {
+#pragma unroll
+        for (int j = 0; j < kIter; ++j) {
+          const int e = 16 * (t0 + j * kStep);
+          uint4 zh, zm, zl;
+          split3(*reinterpret_cast<const uint4 *>(zt + e), wf[j], zh, zm, zl);
+          *reinterpret_cast<uint4 *>(zw + e) = zh;
+          *reinterpret_cast<uint4 *>(zw + L::kZTile + e) = zm;
+          *reinterpret_cast<uint4 *>(zw + 2 * L::kZTile + e) = zl;
+        }
+      } else if (ok) {
+        // rows behind the sequence hold anything, and zero times it must not be NaN: those
+        // that the products read are cleared
+        const int m16 = (m + 15) & ~15;
+        for (int u = t0; u < m16 * 8; u += kStep) {
+          const int r = u >> 3, e = 16 * u;
+          uint4 zh, zm, zl, a = *reinterpret_cast<const uint4 *>(zt + e);
+          if (r >= m) {
+            a = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(zt + e) = a;
+          }
+          split3(a, W[r < m ? (REV ? r + 1 : m - 1 - r) : 0], zh, zm, zl);
+          *reinterpret_cast<uint4 *>(zw + e) = zh;
+          *reinterpret_cast<uint4 *>(zw + L::kZTile + e) = zm;
+          *reinterpret_cast<uint4 *>(zw + 2 * L::kZTile + e) = zl;
+        }
+        const int dead = (m16 - m) * 8;
+        for (int kb = 0; kb < KB; ++kb) {
+          const int sy = slot(i, kb);
+          if (ok) ok = dev::mbar_wait(&yfull[sy], phase(i, kb), w.status);
+          if (!ok) break;
+          for (int u = t0; u < dead * kblocks_of(kb); u += kStep)
+            *reinterpret_cast<uint4 *>(smem + L::y + sy * L::kTile + (u / dead) * kC * 128 + m * 128 + (u % dead) * 16) =
+                make_uint4(0, 0, 0, 0);
+        }
+      }
+      dev::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) dev::mbar_arrive(zready);
+    }
+  };
+
+  if (warp < 4) {
+    dev::regs_dec<R::roles>();
+    if (warp == 0) {
     // ============================ loads ============================
     if (lane == 0 && nloc > 0) {
       bool ok = true;
@@ -213,165 +289,141 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = max(0, xl - 2); j < xl; ++j) (void)dev::mbar_wait(&xfull[j & 1], (uint32_t)((j >> 1) & 1), w.status);
       for (int j = max(0, zl - NZ); j < zl; ++j) (void)dev::mbar_wait(&zfull[j % NZ], (uint32_t)((j / NZ) & 1), w.status);
     }
-  } else if (warp == 1) {
+    } else if (warp == 1) {
     // ============================ products ============================
-    if (lane == 0) {
-      constexpr uint32_t id_sc = dev::idesc_bf16(kC, kC, false, false);   // X, Y: K-major
-      constexpr uint32_t id_o = dev::idesc_bf16(kC, kBV, false, true);    // X or P (TMEM); S or Z: MN-major
-      constexpr uint32_t id_ds = dev::idesc_bf16(128, kDsCols, true, true);  // Y, Zw: MN-major
-      constexpr uint32_t id_dl = dev::idesc_bf16(128, kBV, true, true);
-      const uint32_t sX = dev::smem_u32(smem + L::x), sY = dev::smem_u32(smem + L::y), sZ = dev::smem_u32(smem + L::z),
-                     sS = dev::smem_u32(smem + L::s), sZw = dev::smem_u32(smem + L::zw);
-      bool ok = true;
-      // X Y^T of chunk i
-      auto scores = [&](int i) {
+    // the whole warp runs the loop (all of it is warp-uniform), one thread issues
+    constexpr uint32_t id_sc = dev::idesc_bf16(kC, kC, false, false);   // X, Y: K-major
+    constexpr uint32_t id_o = dev::idesc_bf16(kC, kBV, false, true);    // X or P (TMEM); S or Z: MN-major
+    constexpr uint32_t id_dh = dev::idesc_bf16(128, 2 * kBV, true, true);  // Y, two parts of Zw: MN-major
+    constexpr uint32_t id_dl = dev::idesc_bf16(128, kBV, true, true);
+    // descriptors of a tile's first step; step kk lies koff(kk) (K-major) or mnoff(kk) further
+    const uint64_t dX = dev::desc_kmajor(dev::smem_u32(smem + L::x), kC, 0, 0),
+                   dYk = dev::desc_kmajor(dev::smem_u32(smem + L::y), kC, 0, 0),
+                   dYm = dev::desc_mnmajor(dev::smem_u32(smem + L::y), kC, 0, 0),
+                   dZ = dev::desc_mnmajor(dev::smem_u32(smem + L::z), kC, 0, 0),
+                   dS = dev::desc_mnmajor(dev::smem_u32(smem + L::s), 128 * KB, 0, 0),
+                   dZw = dev::desc_mnmajor(dev::smem_u32(smem + L::zw), kC, 0, 0);
+    constexpr auto koff = [](int kk) { return (uint64_t)(((kk >> 2) * kC * 128 + (kk & 3) * 32) >> 4); };
+    constexpr auto mnoff = [](int kk) { return (uint64_t)((kk * 16 * 128) >> 4); };
+    constexpr uint64_t kTileD = L::kTile >> 4, kZTileD = L::kZTile >> 4;
+    const bool leader = dev::elect_one();
+    auto wait = [&](uint64_t *bar, uint32_t par) { return __all_sync(0xffffffffu, dev::mbar_wait(bar, par, w.status)) != 0; };
+    bool ok = true;
+    // X Y^T of chunk i
+    auto scores = [&](int i) {
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-          const int s = slot(i, kb);
-          ok = ok && dev::mbar_wait(&xfull[s], phase(i, kb), w.status) && dev::mbar_wait(&yfull[s], phase(i, kb), w.status);
-          if (!ok) return;
-          dev::tc_fence_after();
-          const int ks = ksteps_of(kb);
-          for (int kk = 0; kk < ks; ++kk)
-            dev::umma_bf16(tmem + kColSc, dev::desc_kmajor(sX + s * L::kTile, kC, 0, kk * 16),
-                           dev::desc_kmajor(sY + s * L::kTile, kC, 0, kk * 16), id_sc, kb + kk > 0 ? 1u : 0u);
+      for (int kb = 0; kb < KB; ++kb) {
+        const int s = slot(i, kb);
+        ok = ok && wait(&xfull[s], phase(i, kb)) && wait(&yfull[s], phase(i, kb));
+        if (!ok) return;
+        dev::tc_fence_after();
+        const int ks = ksteps_of(kb);
+        const uint64_t x = dX + s * kTileD, y = dYk + s * kTileD;
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            if (kk < ks) dev::umma_bf16(tmem + kColSc, x + koff(kk), y + koff(kk), id_sc, kb + kk > 0 ? 1u : 0u);
           if (KB == 2) dev::umma_commit(&xempty[s]);  // X S came first
+          if (kb == KB - 1) dev::umma_commit(scfull);
         }
-        dev::umma_commit(scfull);
-      };
-      // X S of chunk i
-      auto inter = [&](int i) {
-        ok = ok && dev::mbar_wait(sfull, (uint32_t)(i & 1), w.status);
-        if (ok && i > 0) ok = dev::mbar_wait(oempty, (uint32_t)((i & 1) ^ 1), w.status);
+        __syncwarp();
+      }
+    };
+    // X S of chunk i
+    auto inter = [&](int i) {
+      ok = ok && wait(sfull, (uint32_t)(i & 1));
+      if (ok && i > 0) ok = wait(oempty, (uint32_t)((i & 1) ^ 1));
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-          const int s = slot(i, kb);
-          ok = ok && dev::mbar_wait(&xfull[s], phase(i, kb), w.status);
-          if (!ok) return;
-          dev::tc_fence_after();
-          const int ks = ksteps_of(kb);
-          for (int kk = 0; kk < ks; ++kk)
-            dev::umma_bf16(tmem + kColOb, dev::desc_kmajor(sX + s * L::kTile, kC, 0, kk * 16),
-                           dev::desc_mnmajor(sS, 128 * KB, 128 * kb + kk * 16, 0), id_o, kb + kk > 0 ? 1u : 0u);
+      for (int kb = 0; kb < KB; ++kb) {
+        const int s = slot(i, kb);
+        ok = ok && wait(&xfull[s], phase(i, kb));
+        if (!ok) return;
+        dev::tc_fence_after();
+        const int ks = ksteps_of(kb);
+        const uint64_t x = dX + s * kTileD;
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            if (kk < ks) dev::umma_bf16(tmem + kColOb, x + koff(kk), dS + mnoff(8 * kb + kk), id_o, kb + kk > 0 ? 1u : 0u);
           if (KB == 1) dev::umma_commit(&xempty[s]);  // X Y^T came first
+          if (kb == KB - 1) dev::umma_commit(qsdone);
         }
-        dev::umma_commit(qsdone);
-      };
-      for (int i = 0; i < nloc && ok; ++i) {
-        const uint32_t par = (uint32_t)(i & 1);
-        const int tsteps = (live_of(i) + 15) / 16;  // 16-token steps that hold a live token
-        // With 128 channels X Y^T goes first, so that P is ready by the time dS is done; with
-        // 256 X S does, while the next Y, which has no second buffer, arrives.
-        if (OUT) {
-          if (KB == 1) {
-            scores(i);
-            inter(i);
-          } else {
-            inter(i);
-            scores(i);
-          }
+        __syncwarp();
+      }
+    };
+    for (int i = 0; i < nloc && ok; ++i) {
+      const uint32_t par = (uint32_t)(i & 1);
+      const int ts = (live_of(i) + 15) / 16;  // 16-token steps that hold a live token
+      // With 128 channels X Y^T goes first, so that P is ready by the time dS is done; with
+      // 256 X S does, while the next Y, which has no second buffer, arrives.
+      if (OUT) {
+        if (KB == 1) {
+          scores(i);
+          inter(i);
+        } else {
+          inter(i);
+          scores(i);
         }
-        ok = ok && dev::mbar_wait(&zfull[i % NZ], (uint32_t)((i / NZ) & 1), w.status) &&
-             dev::mbar_wait(zready, par, w.status);
-        if (ok && i > 0) ok = dev::mbar_wait(dsempty, par ^ 1u, w.status);
-        if (!ok) break;
+      }
+      ok = ok && wait(&zfull[i % NZ], (uint32_t)((i / NZ) & 1)) && wait(zready, par);
+      if (ok && i > 0) ok = wait(dsempty, par ^ 1u);
+      if (!ok) break;
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-          const int s = slot(i, kb);
-          ok = ok && dev::mbar_wait(&yfull[s], phase(i, kb), w.status);
-          if (!ok) break;
-          dev::tc_fence_after();
-          for (int kk = 0; kk < tsteps; ++kk) {
-            const uint64_t dy = dev::desc_mnmajor(sY + s * L::kTile, kC, kk * 16, 0);
-            dev::umma_bf16(tmem + kColDs + kb * 128, dy, dev::desc_mnmajor(sZw, kC, kk * 16, 0), id_ds, kk > 0 ? 1u : 0u);
-            if (KB == 2)
-              dev::umma_bf16(tmem + kColDs + kb * 128 + kBV, dy, dev::desc_mnmajor(sZw + 2 * L::kZTile, kC, kk * 16, 0),
-                             id_dl, 1u);
-          }
-          dev::umma_commit(&yempty[s]);
-        }
+      for (int kb = 0; kb < KB; ++kb) {
+        const int s = slot(i, kb);
+        ok = ok && wait(&yfull[s], phase(i, kb));
         if (!ok) break;
-        dev::umma_commit(dsfull);
+        dev::tc_fence_after();
+        const uint64_t y = dYm + s * kTileD;
+        const uint32_t d = tmem + kColDs + kb * 128;
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            if (kk < ts) {
+              dev::umma_bf16(d, y + mnoff(kk), dZw + mnoff(kk), id_dh, kk > 0 ? 1u : 0u);
+              dev::umma_bf16(d + kBV, y + mnoff(kk), dZw + 2 * kZTileD + mnoff(kk), id_dl, 1u);
+            }
+          dev::umma_commit(&yempty[s]);
+          if (kb == KB - 1) dev::umma_commit(dsfull);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (OUT) {
+        ok = wait(pfull, par);
+        if (!ok) break;
+        dev::tc_fence_after();
+      }
+      if (leader) {
+        const uint64_t z = dZ + (i % NZ) * kZTileD;
         if (OUT) {
-          ok = dev::mbar_wait(pfull, par, w.status);
-          if (!ok) break;
-          dev::tc_fence_after();
-          for (int kk = 0; kk < tsteps; ++kk)
-            dev::umma_bf16_ts(tmem + kColOa, tmem + kColSc + kk * 8,
-                              dev::desc_mnmajor(sZ + (i % NZ) * L::kZTile, kC, kk * 16, 0), id_o, kk > 0 ? 1u : 0u);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            if (kk < ts) dev::umma_bf16_ts(tmem + kColOa, tmem + kColSc + kk * 8, z + mnoff(kk), id_o, kk > 0 ? 1u : 0u);
           dev::umma_commit(ofull);
         }
         dev::umma_commit(&zempty[i % NZ]);
       }
+      __syncwarp();
+    }
+    if (leader) {
       dev::umma_commit(done);  // all products have completed before TMEM is released
       (void)dev::mbar_wait(done, 0, w.status);
     }
-  } else if (warp >= kScale0 && warp < kScale0 + kScaleWarps) {
-    // ============================ w (.) Z ============================
-    const int t0 = tid - 32 * kScale0;
-    constexpr int kStep = 32 * kScaleWarps, kIter = kC * 8 / kStep;  // 16-byte units per pass, passes
-    bool ok = true;
-    float wf[kIter];  // the weights of a whole chunk: this thread's rows are t0 / 8 + (kStep / 8) j
-#pragma unroll
-    for (int j = 0; j < kIter; ++j) {
-      const int r = (t0 + j * kStep) >> 3;
-      wf[j] = W[w.reverse ? r + 1 : kC - 1 - r];
+    __syncwarp();
+    } else if (KB == 2) {
+      scale_z();
     }
-    for (int i = 0; i < nloc; ++i) {
-      const int s = i % NZ;
-      const int m = live_of(i);
-      if (ok) ok = dev::mbar_wait(&zfull[s], (uint32_t)((i / NZ) & 1), w.status);
-      if (ok && i > 0) ok = dev::mbar_wait(dsfull, (uint32_t)((i - 1) & 1), w.status);
-      uint8_t *zt = smem + L::z + s * L::kZTile, *zw = smem + L::zw;
-      // a row is eight 16-byte units; their place in the swizzled row does not matter here
-      if (ok && m == kC) {
-#pragma unroll
-        for (int j = 0; j < kIter; ++j) {
-          const int e = 16 * (t0 + j * kStep);
-          uint4 zh, zm, zl;
-          split3(*reinterpret_cast<const uint4 *>(zt + e), wf[j], zh, zm, zl);
-          *reinterpret_cast<uint4 *>(zw + e) = zh;
-          *reinterpret_cast<uint4 *>(zw + L::kZTile + e) = zm;
-          *reinterpret_cast<uint4 *>(zw + 2 * L::kZTile + e) = zl;
-        }
-      } else if (ok) {
-        // rows behind the sequence hold anything, and zero times it must not be NaN: those
-        // that the products read are cleared
-        const int m16 = (m + 15) & ~15;
-        for (int u = t0; u < m16 * 8; u += kStep) {
-          const int r = u >> 3, e = 16 * u;
-          uint4 zh, zm, zl, a = *reinterpret_cast<const uint4 *>(zt + e);
-          if (r >= m) {
-            a = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4 *>(zt + e) = a;
-          }
-          split3(a, W[r < m ? (w.reverse ? r + 1 : m - 1 - r) : 0], zh, zm, zl);
-          *reinterpret_cast<uint4 *>(zw + e) = zh;
-          *reinterpret_cast<uint4 *>(zw + L::kZTile + e) = zm;
-          *reinterpret_cast<uint4 *>(zw + 2 * L::kZTile + e) = zl;
-        }
-        const int dead = (m16 - m) * 8;
-        for (int kb = 0; kb < KB; ++kb) {
-          const int sy = slot(i, kb);
-          if (ok) ok = dev::mbar_wait(&yfull[sy], phase(i, kb), w.status);
-          if (!ok) break;
-          for (int u = t0; u < dead * kblocks_of(kb); u += kStep)
-            *reinterpret_cast<uint4 *>(smem + L::y + sy * L::kTile + (u / dead) * kC * 128 + m * 128 + (u % dead) * 16) =
-                make_uint4(0, 0, 0, 0);
-        }
-      }
-      dev::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) dev::mbar_arrive(zready);
-    }
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp < 8) {
     // ============================ P and O ============================
+    dev::regs_inc<R::rows>();
     if (OUT) {
       const int q4 = warp & 3, t = 32 * q4 + lane;
       const uint32_t lane_base = tmem + ((uint32_t)(32 * q4) << 16);
       const long rows = w.packed ? w.T : (long)w.nseq * w.T;
       const bool wide = (((uintptr_t)w.o.p | (uintptr_t)(2 * w.o.st) | (uintptr_t)(2 * w.o.sh) | (uintptr_t)(2 * w.o.sb)) & 31u) == 0;
       const int nv = min(kBV, w.V - v0);  // a multiple of 8
+      const float *col = REV ? W : Wr;
       bool ok = true;
       for (int i = 0; i < nloc; ++i) {
         const uint32_t par = (uint32_t)(i & 1);
@@ -379,50 +431,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long row0 = sq.row0 + (long)chunk_of(i) * kC;
         if (ok) ok = dev::mbar_wait(scfull, par, w.status);
         dev::tc_fence_after();
-        // 32 columns (tokens j) at a time.  P's columns 16 jb .. lie over scores that this
-        // warp has read.  Blocks on the far side of the diagonal are zero.  On the near side
-        // the weight is one factor per thread times one per column: forward
+        // 64 columns (tokens j) at a time.  P's columns 32 jp .. lie over scores that this
+        // warp has read.  Blocks of 32 on the far side of the diagonal are zero.  On the near
+        // side the weight is one factor per thread times one per column: forward
         // lambda^(t-j) = lambda^(t - 32 jb - 31) lambda^(31 - e), j = 32 jb + e, reverse
         // lambda^(j-t) = lambda^(32 jb - t) lambda^e.
 #pragma unroll 1
-        for (int jb = 0; jb < 4; ++jb) {
-          uint32_t p[16];
-          if (w.reverse ? jb < q4 : jb > q4) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) p[e] = 0u;
-          } else {
-            float sc[32];
-            dev::tmem_ld32(lane_base + kColSc + 32 * jb, sc);
-            const float *col = w.reverse ? W : Wr;
-            const float a = W[jb == q4 ? 0 : (w.reverse ? 32 * jb - t : t - 32 * jb - 31)];
-            float f[32];
-            if (jb == q4) {
-              // the diagonal block: |lane - e| steps apart; what lies beyond it is not
-              // multiplied by zero but replaced, it may be anything
-#pragma unroll
-              for (int e = 0; e < 32; ++e) f[e] = W[abs(lane - e)];
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 c = *reinterpret_cast<const float4 *>(col + e);
-                f[e] = a * c.x, f[e + 1] = a * c.y, f[e + 2] = a * c.z, f[e + 3] = a * c.w;
-              }
-            }
+        for (int jp = 0; jp < 2; ++jp) {
+          const bool dead = REV ? 2 * jp + 1 < q4 : 2 * jp > q4;
+          float sc[64];
+          if (!dead) {
+            dev::tmem_ld32(lane_base + kColSc + 64 * jp, sc);
+            dev::tmem_ld32(lane_base + kColSc + 64 * jp + 32, sc + 32);
             dev::tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) sc[e] *= f[e];
-            if (jb == q4) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) sc[e] = (w.reverse ? e >= lane : e <= lane) ? sc[e] : 0.f;
-            }
-            if (w.reverse && m < kC) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) sc[e] = 32 * jb + e < m ? sc[e] : 0.f;
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) p[e] = dev::pack_bf16(sc[2 * e], sc[2 * e + 1]);
           }
-          dev::tmem_st16u(lane_base + kColSc + 16 * jb, p);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int jb = 2 * jp + u;
+            uint32_t p[16];
+            if (REV ? jb < q4 : jb > q4) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) p[e] = 0u;
+            } else {
+              if (jb == q4) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) sc[32 * u + e] *= REV ? Wd[31 - lane + e] : Wd[31 + lane - e];
+              } else {
+                const float a = W[REV ? 32 * jb - t : t - 32 * jb - 31];
+                const dev::f2 a2 = dev::pk(a, a);
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                  const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(col + e);
+                  float *x = sc + 32 * u + e;
+                  dev::upk(dev::mul2(dev::pk(x[0], x[1]), dev::mul2(a2, c.x)), x[0], x[1]);
+                  dev::upk(dev::mul2(dev::pk(x[2], x[3]), dev::mul2(a2, c.y)), x[2], x[3]);
+                }
+              }
+              if (m < kC) {  // rows behind the sequence hold anything: replaced, not multiplied
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  const int j = 32 * jb + e;
+                  sc[32 * u + e] = (REV ? j >= t && j < m : j <= t) ? sc[32 * u + e] : 0.f;
+                }
+              }
+#pragma unroll
+              for (int e = 0; e < 16; ++e) p[e] = dev::pack_bf16(sc[32 * u + 2 * e], sc[32 * u + 2 * e + 1]);
+            }
+            dev::tmem_st16u(lane_base + kColSc + 16 * jb, p);
+          }
         }
         dev::tmem_wait_st();
         dev::tc_fence_before();
@@ -431,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         if (ok) ok = dev::mbar_wait(ofull, par, w.status);
         dev::tc_fence_after();
-        const float f = W[t < m ? (w.reverse ? m - 1 - t : t + 1) : 0];
+        const float f = W[t < m ? (REV ? m - 1 - t : t + 1) : 0];
         __nv_bfloat16 *o = (__nv_bfloat16 *)w.o.p + sq.b * w.o.sb + h * w.o.sh + (row0 + t) * w.o.st + v0;
         const bool live = t < m && ok;
 #pragma unroll
@@ -445,10 +501,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) dev::mbar_arrive(oempty);
           }
+          const dev::f2 f2v = dev::pk(f, f);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) a[e] = fmaf(f, c[e], a[e]);
-          if (!live) continue;
-          if (w.acc_in || w.acc_out) {
+          for (int e = 0; e < 32; e += 2)
+            dev::upk(dev::fma2(f2v, dev::pk(c[e], c[e + 1]), dev::pk(a[e], a[e + 1])), a[e], a[e + 1]);
+          if (live && (w.acc_in || w.acc_out)) {
             const long row = w.packed ? row0 + t : (long)b * w.T + row0 + t;
             float *part = w.acc + ((long)h * rows + row) * w.V + v0 + 32 * hf;
 #pragma unroll
@@ -462,11 +519,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (w.acc_out) *reinterpret_cast<float4 *>(part + e) = x;
               }
-            if (w.acc_out) continue;
           }
           uint32_t r[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) r[e] = dev::pack_bf16(a[2 * e], a[2 * e + 1]);
+          if (!live || w.acc_out) continue;
           if (wide && nv == kBV) {
             st_global_32(o + 32 * hf, r);
             st_global_32(o + 32 * hf + 16, r + 8);
@@ -480,8 +537,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp >= 8 && warp < 8 + kStateWarps) {
+  } else if (warp < 8 + kStateWarps) {
     // ============================ state ============================
+    if (KB == 1) dev::regs_inc<R::state>();
     const int q4 = warp & 3, kb = (warp - 8) >> 2, kr = 128 * kb + 32 * q4 + lane;  // this thread's channel
     const uint32_t lane_base = tmem + ((uint32_t)(32 * q4) << 16);
     const long KV = (long)w.K * w.V;
@@ -554,24 +612,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ok) ok = dev::mbar_wait(dsfull, (uint32_t)(i & 1), w.status);
       dev::tc_fence_after();
-      // the parts of dS 16 columns at a time, the small ones added first
+      // kCols columns at a time, the small part of dS added first
+      constexpr int kCols = KB == 1 ? 32 : 16;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        float d0[16], d1[16], d2[16];
-        const uint32_t c = lane_base + kColDs + kb * 128 + 16 * g;
-        dev::tmem_ld16(c, d0);
-        dev::tmem_ld16(c + kBV, d1);
-        if (KB == 1) dev::tmem_ld16(c + 2 * kBV, d2);
+      for (int g = 0; g < kBV / kCols; ++g) {
+        float d0[kCols], d1[kCols];
+        const uint32_t c = lane_base + kColDs + kb * 128 + kCols * g;
+        if (KB == 1) {
+          dev::tmem_ld32(c, d0);
+          dev::tmem_ld32(c + kBV, d1);
+        } else {
+          dev::tmem_ld16(c, d0);
+          dev::tmem_ld16(c + kBV, d1);
+        }
         dev::tmem_wait_ld();
-        if (g == 3) {
+        if (g == kBV / kCols - 1) {
           dev::tc_fence_before();
           __syncwarp();
           if (lane == 0) dev::mbar_arrive(dsempty);
         }
+        const dev::f2 dh2 = dev::pk(dh, dh), dl2 = dev::pk(dl, dl);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float lo = KB == 1 ? d2[e] + d1[e] : d1[e];
-          S[16 * g + e] = fmaf(S[16 * g + e], dh, fmaf(S[16 * g + e], dl, lo) + d0[e]);
+        for (int e = 0; e < kCols; e += 2) {
+          float *x = S + kCols * g + e;
+          const dev::f2 old = dev::pk(x[0], x[1]);
+          const dev::f2 lo = dev::fma2(old, dl2, dev::pk(d1[e], d1[e + 1]));
+          dev::upk(dev::fma2(old, dh2, dev::add2(lo, dev::pk(d0[e], d0[e + 1]))), x[0], x[1]);
         }
       }
       if (OUT && i + 1 < nloc) {
@@ -599,6 +665,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+  } else {
+    dev::regs_dec<R::scale>();
+    scale_z();
   }
   dev::tc_fence_before();
   __syncthreads();
@@ -623,19 +692,19 @@ bool make_map(CUtensorMap *m, const DView &v, const DecayWalk &w, int channels) 
   return tc::map4_bf16(m, v.p, dims, strides, 64, kC);
 }
 
-template <int KB>
+template <int KB, bool REV>
 int launch(const DecayWalk &w, cudaStream_t st) {
   CUtensorMap mx, my, mz;
   if (!make_map(&mx, w.x, w, w.K) || !make_map(&my, w.y, w, w.K) || !make_map(&mz, w.z, w, w.V))
     return GLA_ERR_CUDA;
   const int smem = Smem<KB>::bytes + 1024;
-  if (cudaFuncSetAttribute(k_decay_tc<KB, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-      cudaFuncSetAttribute(k_decay_tc<KB, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  if (cudaFuncSetAttribute(k_decay_tc<KB, true, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+      cudaFuncSetAttribute(k_decay_tc<KB, false, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return GLA_ERR_CUDA;
   const unsigned gx = (unsigned)((long)w.nseq * w.H * ((w.V + kBV - 1) / kBV));
   if (w.P > 1)
-    GLA_LAUNCH(K_DECAY_STATES, st, (k_decay_tc<KB, false><<<dim3(gx, w.P - 1), kThreads, smem, st>>>(w, mx, my, mz)));
-  GLA_LAUNCH(K_DECAY_WALK, st, (k_decay_tc<KB, true><<<dim3(gx, w.P), kThreads, smem, st>>>(w, mx, my, mz)));
+    GLA_LAUNCH(K_DECAY_STATES, st, (k_decay_tc<KB, false, REV><<<dim3(gx, w.P - 1), kThreads, smem, st>>>(w, mx, my, mz)));
+  GLA_LAUNCH(K_DECAY_WALK, st, (k_decay_tc<KB, true, REV><<<dim3(gx, w.P), kThreads, smem, st>>>(w, mx, my, mz)));
   return GLA_OK;
 }
 
@@ -648,6 +717,9 @@ bool decay_tc_takes(const DecayWalk &w, int dtype) {
          ok_view(w.z, w) && ok_view(w.o, w);
 }
 
-int decay_walk_tc(const DecayWalk &w, cudaStream_t st) { return w.K <= 128 ? launch<1>(w, st) : launch<2>(w, st); }
+int decay_walk_tc(const DecayWalk &w, cudaStream_t st) { 
+  if (w.reverse) return w.K <= 128 ? launch<1, true>(w, st) : launch<2, true>(w, st);
+  return w.K <= 128 ? launch<1, false>(w, st) : launch<2, false>(w, st);
+ }
 
 }  // namespace gla
