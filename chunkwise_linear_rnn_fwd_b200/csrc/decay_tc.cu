@@ -24,8 +24,9 @@
 // Precision: P and the copy of S that X S reads are rounded to bf16 (2^-8 of each term, the
 // output's own rounding is as large).  The carried state is returned in fp32 and lives on
 // through every later chunk, so its update must not lose that: Y is exact, and w (.) Z is
-// cut into three bf16 values of eight bits each, which is exact.  Two of the three tiles
-// stand side by side, so that one product of N = 128 columns reads Y for both.  lambda^m
+// cut into three bf16 values of eight bits each, which is exact.  The three tiles stand side
+// by side, so that one product of N = 192 columns reads Y once for all (two with 256
+// channels, where TMEM is full: 128 and 64).  lambda^m
 // multiplies the state once a chunk, hundreds of times in a long sequence: it is applied as
 // a sum of two fp32 numbers.
 //
@@ -43,15 +44,15 @@ constexpr int kC = 128;   // tokens of a chunk
 constexpr int kBV = 64;   // columns of V per CTA
 constexpr int kThreads = 512;
 constexpr int kTmemCols = 512;
-// TMEM columns: scores fp32 (then P in bf16), the output accumulators, dS (per 128
-// channels 64 columns for the first part of Zw and 64 for the two others)
+// TMEM columns: scores fp32 (then P in bf16), the output accumulators, dS (64 columns for
+// each part of Zw; with 256 channels 128 per 128, where the two small parts share theirs)
 constexpr uint32_t kColSc = 0, kColOa = 128, kColOb = 192, kColDs = 256;
 
 // Registers a thread, per warpgroup.  Launched with 128; the groups that wait and issue give
 // some to those that hold rows of scores and of the state.
 template <int KB>
 struct Regs {
-  static constexpr int roles = KB == 1 ? 80 : 96, rows = 160, state = KB == 1 ? 168 : 128, scale = 96;
+  static constexpr int roles = 104, rows = 152, state = KB == 1 ? 152 : 128, scale = 104;
   static_assert(roles + rows + (KB == 1 ? state + scale : 2 * state) <= 4 * 128, "more than the launch allocates");
 };
 
@@ -62,7 +63,7 @@ struct Smem {
   static constexpr int kTile = kC * 128 * 2;  // 128 channels of X or Y: two SW128 blocks of 64
   static constexpr int kZTile = kC * kBV * 2;
   static constexpr int x = 0, y = x + 2 * kTile, z = y + 2 * kTile, zw = z + kZStages * kZTile, s = zw + 3 * kZTile,
-                       t = s + 128 * KB * kBV * 2, bar = t + 928, bytes = bar + 256;
+                       t = s + 128 * KB * kBV * 2, bar = t + 528, bytes = bar + 256;
   static_assert(bytes + 1024 <= kMaxDynSmem, "");
 };
 
@@ -104,12 +105,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = Smem<KB>;
   constexpr int NZ = L::kZStages;
   constexpr int kStateWarps = 4 * KB;
-  constexpr int kScale0 = KB == 1 ? 12 : 2, kScaleWarps = KB == 1 ? 4 : 2;
+  // warps of the first warpgroup: a helper reads the rows (TMEM lanes) of its number mod 4,
+  // and the rows that need one are the last 64, in a reverse walk the first
+  constexpr int kLoadWarp = REV ? 2 : 0, kIssueWarp = kLoadWarp + 1, kHelp0 = REV ? 0 : 2;
+  constexpr int kScale0 = KB == 1 ? 12 : kHelp0, kScaleWarps = KB == 1 ? 4 : 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   float *W = (float *)(smem + L::t);  // W[n] = lambda^n, n = 0 .. 128
-  float *Wr = W + 132;                // Wr[e] = lambda^(31-e), e = 0 .. 31
-  float *Wd = Wr + 32;                // Wd[31+n] = lambda^n, n = 0 .. 31; zero below
   uint64_t *bars = (uint64_t *)(smem + L::bar);
   // slot (i KB + kb) mod 2 of X and Y holds channel block kb of chunk i
   uint64_t *xfull = bars, *xempty = xfull + 2, *yfull = xempty + 2, *yempty = yfull + 2, *zfull = yempty + 2,
@@ -123,13 +125,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int vt = blockIdx.x % tiles, seg = blockIdx.y;
   const long bh = blockIdx.x / tiles;
   const int b = (int)(bh / w.H), h = (int)(bh % w.H), v0 = vt * kBV;
+  const int kz = OUT ? 0 : blockIdx.z;  // without outputs, 128 channels a CTA: the first block of these
   if (tid == 0) {
     dev::prefetch_tmap(&tmY);
     dev::prefetch_tmap(&tmZ);
     if (OUT) dev::prefetch_tmap(&tmX);
     for (int i = 0; i < 12; ++i) dev::mbar_init(&xfull[i], 1);
     dev::mbar_init(scfull, 1);
-    dev::mbar_init(pfull, 4);
+    dev::mbar_init(pfull, 6);
     dev::mbar_init(ofull, 1);
     dev::mbar_init(oempty, 4);
     dev::mbar_init(dsfull, 1);
@@ -149,14 +152,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int ksteps = (w.K + 15) / 16, kblocks = (w.K + 63) / 64;
   // of channel block kb: 16-channel steps, 64-column blocks
   auto ksteps_of = [&](int kb) { return min(8, ksteps - 8 * kb); };
-  auto kblocks_of = [&](int kb) { return min(2, kblocks - 2 * kb); };
+  auto kblocks_of = [&](int kb) { return min(2, kblocks - 2 * (kz + kb)); };
   auto slot = [&](int i, int kb) { return (i * KB + kb) & 1; };
   auto phase = [&](int i, int kb) { return (uint32_t)(((i * KB + kb) >> 1) & 1); };
   auto load_y = [&](int i, int kb) {
     const int s = slot(i, kb), row = (int)(sq.row0 + (long)chunk_of(i) * kC);
     dev::mbar_arrive_expect_tx(&yfull[s], (uint32_t)(kblocks_of(kb) * kC * 128));
     for (int cb = 0; cb < kblocks_of(kb); ++cb)
-      dev::tma_load_4d(smem + L::y + s * L::kTile + cb * kC * 128, &tmY, 128 * kb + cb * 64, row, h, sq.b, &yfull[s]);
+      dev::tma_load_4d(smem + L::y + s * L::kTile + cb * kC * 128, &tmY, 128 * (kz + kb) + cb * 64, row, h, sq.b, &yfull[s]);
   };
   auto load_x = [&](int i, int kb) {
     const int s = slot(i, kb), row = (int)(sq.row0 + (long)chunk_of(i) * kC);
@@ -176,14 +179,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     load_z(0);
   }
-  if (warp == 1) dev::tmem_alloc(tslot, kTmemCols);
+  if (warp == kIssueWarp) dev::tmem_alloc(tslot, kTmemCols);
   const double rate = dev::decay_rate(w.ld, h, w.status);
   if (tid >= 128 && tid <= 128 + kC) W[tid - 128] = (float)dev::decay_pow(rate, tid - 128);
-  if (tid >= 320 && tid < 352) {
-    Wr[tid - 320] = (float)dev::decay_pow(rate, 351 - tid);
-    Wd[tid - 289] = (float)dev::decay_pow(rate, tid - 320);
-    if (tid < 351) Wd[tid - 320] = 0.f;
-  }
   int i0, i1;
   dev::decay_slots(w.s0, w.s1, w.alias, w.nseq, b, OUT ? w.status : nullptr, i0, i1);
   dev::tc_fence_before();
@@ -193,37 +191,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   using R = Regs<KB>;
 
   // ============================ w (.) Z ============================
-  auto scale_z = [&]() {
-    const int t0 = tid - 32 * kScale0;
-    constexpr int kStep = 32 * kScaleWarps, kIter = kC * 8 / kStep;  // 16-byte units per pass, passes
-    bool ok = true;
-    float wf[kIter];  // the weights of a whole chunk: this thread's rows are t0 / 8 + (kStep / 8) j
-#pragma unroll
-    for (int j = 0; j < kIter; ++j) {
-      const int r = (t0 + j * kStep) >> 3;
-      wf[j] = W[REV ? r + 1 : kC - 1 - r];
-    }
-    for (int i = 0; i < nloc; ++i) {
+  // w (.) Z of chunk i
+  const int t0 = tid - 32 * kScale0;
+  constexpr int kStep = 32 * kScaleWarps, kIter = kC * 8 / kStep;  // 16-byte units per pass, passes
+  auto scale_z = [&](int i, bool &ok) {
       const int s = i % NZ;
       const int m = live_of(i);
       if (ok) ok = dev::mbar_wait(&zfull[s], (uint32_t)((i / NZ) & 1), w.status);
-      if (ok && i > 0) ok = dev::mbar_wait(dsfull, (uint32_t)((i - 1) & 1), w.status);
       uint8_t *zt = smem + L::z + s * L::kZTile, *zw = smem + L::zw;
       // a row is eight 16-byte units; their place in the swizzled row does not matter here
       if (ok && m == kC) {
+        // units are read eight at a time, before the wait and before the first store
 #pragma unroll
-        for (int j = 0; j < kIter; ++j) {
-          const int e = 16 * (t0 + j * kStep);
+        for (int j0 = 0; j0 < kIter; j0 += 8) {
+        uint4 u[8];
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int r = (t0 + (j0 + j) * kStep) >> 3;
+          f[j] = W[REV ? r + 1 : kC - 1 - r];
+          u[j] = *reinterpret_cast<const uint4 *>(zt + 16 * (t0 + (j0 + j) * kStep));
+        }
+        if (j0 == 0 && i > 0) ok = dev::mbar_wait(dsfull, (uint32_t)((i - 1) & 1), w.status);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int e = 16 * (t0 + (j0 + j) * kStep);
           uint4 zh, zm, zl;
-          split3(*reinterpret_cast<const uint4 *>(zt + e), wf[j], zh, zm, zl);
+          split3(u[j], f[j], zh, zm, zl);
           *reinterpret_cast<uint4 *>(zw + e) = zh;
           *reinterpret_cast<uint4 *>(zw + L::kZTile + e) = zm;
           *reinterpret_cast<uint4 *>(zw + 2 * L::kZTile + e) = zl;
+        }
         }
       } else if (ok) {
         // rows behind the sequence hold anything, and zero times it must not be NaN: those
         // that the products read are cleared
         const int m16 = (m + 15) & ~15;
+        if (i > 0) ok = dev::mbar_wait(dsfull, (uint32_t)((i - 1) & 1), w.status);
         for (int u = t0; u < m16 * 8; u += kStep) {
           const int r = u >> 3, e = 16 * u;
           uint4 zh, zm, zl, a = *reinterpret_cast<const uint4 *>(zt + e);
@@ -249,12 +253,67 @@ __global__ void __launch_bounds__(kThreads, 1)
       dev::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) dev::mbar_arrive(zready);
+  };
+
+  // ============================ P ============================
+  // Row t of P = (X Y^T) (.) D, 32 columns (tokens j = 32 jb + e) a block; a block of P lies
+  // over the first half of its own scores.  On the diagonal the weights are kept in
+  // registers; beside it they are multiplied on from the block's near end, lambda a column,
+  // where `near` is this row's weight: a table in shared memory would wait for the
+  // products, whose operands take all its bandwidth.
+  const float lam1 = W[1];
+  const dev::f2 lam2 = dev::pk(W[2], W[2]), lam8 = dev::pk(W[8], W[8]);
+  auto mask_tail = [&](float *sc, int jb, int t, int m) {
+    // rows behind the sequence hold anything: replaced, not multiplied
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const int j = 32 * jb + e;
+      sc[e] = (REV ? j >= t && j < m : j <= t) ? sc[e] : 0.f;
     }
+  };
+  auto store_p = [&](uint32_t base, const float *sc, int jb) {
+    uint32_t p[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) p[e] = dev::pack_bf16(sc[2 * e], sc[2 * e + 1]);
+    dev::tmem_st16u(base + kColSc + 32 * jb, p);
+  };
+  auto weigh = [&](float *sc, float near) {
+    dev::f2 f[4];  // four pairs of columns in turn
+    f[0] = REV ? dev::pk(near, near * lam1) : dev::pk(near * lam1, near);
+#pragma unroll
+    for (int k = 1; k < 4; ++k) f[k] = dev::mul2(f[k - 1], lam2);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      float *x = sc + (REV ? 2 * k : 30 - 2 * k);
+      dev::upk(dev::mul2(dev::pk(x[0], x[1]), f[k & 3]), x[0], x[1]);
+      if (k < 12) f[k & 3] = dev::mul2(f[k & 3], lam8);
+    }
+  };
+  // the helpers' share: two blocks away from the diagonal
+  auto help_p = [&](int i, bool &ok) {
+    const int q4 = warp & 3, t = 32 * q4 + lane, m = live_of(i), jb0 = REV ? 2 : 0;
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * q4) << 16);
+    if (ok) ok = dev::mbar_wait(scfull, (uint32_t)(i & 1), w.status);
+    dev::tc_fence_after();
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float sc[32];
+      dev::tmem_ld32(lane_base + kColSc + 32 * (jb0 + u), sc);
+      const float near = W[REV ? 32 * (jb0 + u) - t : t - 32 * (jb0 + u) - 31];
+      dev::tmem_wait_ld();
+      weigh(sc, near);
+      if (m < kC) mask_tail(sc, jb0 + u, t, m);
+      store_p(lane_base, sc, jb0 + u);
+    }
+    dev::tmem_wait_st();
+    dev::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) dev::mbar_arrive(pfull);
   };
 
   if (warp < 4) {
     dev::regs_dec<R::roles>();
-    if (warp == 0) {
+    if (warp == kLoadWarp) {
     // ============================ loads ============================
     if (lane == 0 && nloc > 0) {
       bool ok = true;
@@ -289,12 +348,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = max(0, xl - 2); j < xl; ++j) (void)dev::mbar_wait(&xfull[j & 1], (uint32_t)((j >> 1) & 1), w.status);
       for (int j = max(0, zl - NZ); j < zl; ++j) (void)dev::mbar_wait(&zfull[j % NZ], (uint32_t)((j / NZ) & 1), w.status);
     }
-    } else if (warp == 1) {
+    } else if (warp == kIssueWarp) {
     // ============================ products ============================
     // the whole warp runs the loop (all of it is warp-uniform), one thread issues
     constexpr uint32_t id_sc = dev::idesc_bf16(kC, kC, false, false);   // X, Y: K-major
     constexpr uint32_t id_o = dev::idesc_bf16(kC, kBV, false, true);    // X or P (TMEM); S or Z: MN-major
-    constexpr uint32_t id_dh = dev::idesc_bf16(128, 2 * kBV, true, true);  // Y, two parts of Zw: MN-major
+    constexpr uint32_t id_dh = dev::idesc_bf16(128, (KB == 1 ? 3 : 2) * kBV, true, true);  // Y, parts of Zw: MN-major
     constexpr uint32_t id_dl = dev::idesc_bf16(128, kBV, true, true);
     // descriptors of a tile's first step; step kk lies koff(kk) (K-major) or mnoff(kk) further
     const uint64_t dX = dev::desc_kmajor(dev::smem_u32(smem + L::x), kC, 0, 0),
@@ -354,17 +413,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < nloc && ok; ++i) {
       const uint32_t par = (uint32_t)(i & 1);
       const int ts = (live_of(i) + 15) / 16;  // 16-token steps that hold a live token
-      // With 128 channels X Y^T goes first, so that P is ready by the time dS is done; with
-      // 256 X S does, while the next Y, which has no second buffer, arrives.
-      if (OUT) {
-        if (KB == 1) {
-          scores(i);
-          inter(i);
-        } else {
-          inter(i);
-          scores(i);
-        }
-      }
+      // With 128 channels X S goes last but one: the state that it reads is made from dS of the
+      // chunk before, and P is ready by then.  With 256 channels it goes first, while the
+      // next Y, which has no second buffer, arrives.
+      if (OUT && KB == 2) inter(i);
+      if (OUT) scores(i);
       ok = ok && wait(&zfull[i % NZ], (uint32_t)((i / NZ) & 1)) && wait(zready, par);
       if (ok && i > 0) ok = wait(dsempty, par ^ 1u);
       if (!ok) break;
@@ -381,13 +434,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < 8; ++kk)
             if (kk < ts) {
               dev::umma_bf16(d, y + mnoff(kk), dZw + mnoff(kk), id_dh, kk > 0 ? 1u : 0u);
-              dev::umma_bf16(d + kBV, y + mnoff(kk), dZw + 2 * kZTileD + mnoff(kk), id_dl, 1u);
+              if (KB == 2) dev::umma_bf16(d + kBV, y + mnoff(kk), dZw + 2 * kZTileD + mnoff(kk), id_dl, 1u);
             }
           dev::umma_commit(&yempty[s]);
           if (kb == KB - 1) dev::umma_commit(dsfull);
         }
         __syncwarp();
       }
+      if (!ok) break;
+      if (OUT && KB == 1) inter(i);
       if (!ok) break;
       if (OUT) {
         ok = wait(pfull, par);
@@ -399,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (OUT) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            if (kk < ts) dev::umma_bf16_ts(tmem + kColOa, tmem + kColSc + kk * 8, z + mnoff(kk), id_o, kk > 0 ? 1u : 0u);
+            if (kk < ts) dev::umma_bf16_ts(tmem + kColOa, tmem + kColSc + 32 * (kk >> 1) + 8 * (kk & 1), z + mnoff(kk), id_o, kk > 0 ? 1u : 0u);
           dev::umma_commit(ofull);
         }
         dev::umma_commit(&zempty[i % NZ]);
@@ -411,8 +466,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       (void)dev::mbar_wait(done, 0, w.status);
     }
     __syncwarp();
-    } else if (KB == 2) {
-      scale_z();
+    } else {
+      bool ok = true;
+      for (int i = 0; i < nloc; ++i) {
+        if (KB == 2) scale_z(i, ok);
+        if (OUT) help_p(i, ok);
+      }
     }
   } else if (warp < 8) {
     // ============================ P and O ============================
@@ -423,7 +482,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long rows = w.packed ? w.T : (long)w.nseq * w.T;
       const bool wide = (((uintptr_t)w.o.p | (uintptr_t)(2 * w.o.st) | (uintptr_t)(2 * w.o.sh) | (uintptr_t)(2 * w.o.sb)) & 31u) == 0;
       const int nv = min(kBV, w.V - v0);  // a multiple of 8
-      const float *col = REV ? W : Wr;
+      const int jo = q4 ^ 1;  // the block beside the diagonal's: on the near or the far side
+      const bool beside = REV ? (q4 & 1) == 0 : (q4 & 1) == 1;
+      const bool clear = REV ? q4 >= 2 : q4 < 2;  // the other two blocks: zero, or a helper's
+      const float near = W[REV ? 32 - lane : lane + 1];
+      float fd[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        const int g = REV ? e - lane : lane - e;
+        fd[e] = g >= 0 ? W[g] : 0.f;
+      }
       bool ok = true;
       for (int i = 0; i < nloc; ++i) {
         const uint32_t par = (uint32_t)(i & 1);
@@ -431,54 +499,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long row0 = sq.row0 + (long)chunk_of(i) * kC;
         if (ok) ok = dev::mbar_wait(scfull, par, w.status);
         dev::tc_fence_after();
-        // 64 columns (tokens j) at a time.  P's columns 32 jp .. lie over scores that this
-        // warp has read.  Blocks of 32 on the far side of the diagonal are zero.  On the near
-        // side the weight is one factor per thread times one per column: forward
-        // lambda^(t-j) = lambda^(t - 32 jb - 31) lambda^(31 - e), j = 32 jb + e, reverse
-        // lambda^(j-t) = lambda^(32 jb - t) lambda^e.
-#pragma unroll 1
-        for (int jp = 0; jp < 2; ++jp) {
-          const bool dead = REV ? 2 * jp + 1 < q4 : 2 * jp > q4;
-          float sc[64];
-          if (!dead) {
-            dev::tmem_ld32(lane_base + kColSc + 64 * jp, sc);
-            dev::tmem_ld32(lane_base + kColSc + 64 * jp + 32, sc + 32);
-            dev::tmem_wait_ld();
-          }
+        float sc[32];
+        dev::tmem_ld32(lane_base + kColSc + 32 * q4, sc);
+        dev::tmem_wait_ld();
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int jb = 2 * jp + u;
-            uint32_t p[16];
-            if (REV ? jb < q4 : jb > q4) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) p[e] = 0u;
-            } else {
-              if (jb == q4) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) sc[32 * u + e] *= REV ? Wd[31 - lane + e] : Wd[31 + lane - e];
-              } else {
-                const float a = W[REV ? 32 * jb - t : t - 32 * jb - 31];
-                const dev::f2 a2 = dev::pk(a, a);
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                  const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(col + e);
-                  float *x = sc + 32 * u + e;
-                  dev::upk(dev::mul2(dev::pk(x[0], x[1]), dev::mul2(a2, c.x)), x[0], x[1]);
-                  dev::upk(dev::mul2(dev::pk(x[2], x[3]), dev::mul2(a2, c.y)), x[2], x[3]);
-                }
-              }
-              if (m < kC) {  // rows behind the sequence hold anything: replaced, not multiplied
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  const int j = 32 * jb + e;
-                  sc[32 * u + e] = (REV ? j >= t && j < m : j <= t) ? sc[32 * u + e] : 0.f;
-                }
-              }
-#pragma unroll
-              for (int e = 0; e < 16; ++e) p[e] = dev::pack_bf16(sc[32 * u + 2 * e], sc[32 * u + 2 * e + 1]);
-            }
-            dev::tmem_st16u(lane_base + kColSc + 16 * jb, p);
-          }
+        for (int e = 0; e < 32; e += 2)
+          dev::upk(dev::mul2(dev::pk(sc[e], sc[e + 1]), dev::pk(fd[e], fd[e + 1])), sc[e], sc[e + 1]);
+        if (m < kC) mask_tail(sc, q4, t, m);
+        store_p(lane_base, sc, q4);
+        if (beside) {
+          dev::tmem_ld32(lane_base + kColSc + 32 * jo, sc);
+          dev::tmem_wait_ld();
+          weigh(sc, near);
+          if (m < kC) mask_tail(sc, jo, t, m);
+          store_p(lane_base, sc, jo);
+        } else {
+          const uint32_t zero[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+          dev::tmem_st16u(lane_base + kColSc + 32 * jo, zero);
+        }
+        if (clear) {
+          const uint32_t zero[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+          dev::tmem_st16u(lane_base + kColSc + 32 * (REV ? 0 : 2), zero);
+          dev::tmem_st16u(lane_base + kColSc + 32 * (REV ? 1 : 3), zero);
         }
         dev::tmem_wait_st();
         dev::tc_fence_before();
@@ -540,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 8 + kStateWarps) {
     // ============================ state ============================
     if (KB == 1) dev::regs_inc<R::state>();
-    const int q4 = warp & 3, kb = (warp - 8) >> 2, kr = 128 * kb + 32 * q4 + lane;  // this thread's channel
+    const int q4 = warp & 3, kb = (warp - 8) >> 2, kc = 128 * kb + 32 * q4 + lane, kr = 128 * kz + kc;  // this thread's channel (of the CTA's, of all)
     const uint32_t lane_base = tmem + ((uint32_t)(32 * q4) << 16);
     const long KV = (long)w.K * w.V;
     float *wsb = w.ws + bh * w.P * KV + (long)kr * w.V + v0;
@@ -587,11 +629,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    const uint32_t srow = dev::smem_u32(smem + L::s) + (uint32_t)kr * 128u;
+    const uint32_t srow = dev::smem_u32(smem + L::s) + (uint32_t)kc * 128u;
     auto publish = [&]() {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        dev::st_shared_v4(srow + (uint32_t)((j ^ (kr & 7)) << 4), dev::pack_bf16(S[8 * j], S[8 * j + 1]),
+        dev::st_shared_v4(srow + (uint32_t)((j ^ (kc & 7)) << 4), dev::pack_bf16(S[8 * j], S[8 * j + 1]),
                           dev::pack_bf16(S[8 * j + 2], S[8 * j + 3]), dev::pack_bf16(S[8 * j + 4], S[8 * j + 5]),
                           dev::pack_bf16(S[8 * j + 6], S[8 * j + 7]));
       dev::fence_proxy_async_smem();
@@ -612,32 +654,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ok) ok = dev::mbar_wait(dsfull, (uint32_t)(i & 1), w.status);
       dev::tc_fence_after();
-      // kCols columns at a time, the small part of dS added first
-      constexpr int kCols = KB == 1 ? 32 : 16;
+      // 16 columns at a time, all of their parts in one trip; the small ones are added first
 #pragma unroll
-      for (int g = 0; g < kBV / kCols; ++g) {
-        float d0[kCols], d1[kCols];
-        const uint32_t c = lane_base + kColDs + kb * 128 + kCols * g;
-        if (KB == 1) {
-          dev::tmem_ld32(c, d0);
-          dev::tmem_ld32(c + kBV, d1);
-        } else {
-          dev::tmem_ld16(c, d0);
-          dev::tmem_ld16(c + kBV, d1);
-        }
+      for (int g = 0; g < 4; ++g) {
+        float d0[16], d1[16], d2[16];
+        const uint32_t c = lane_base + kColDs + kb * 128 + 16 * g;
+        dev::tmem_ld16(c, d0);
+        dev::tmem_ld16(c + kBV, d1);
+        if (KB == 1) dev::tmem_ld16(c + 2 * kBV, d2);
         dev::tmem_wait_ld();
-        if (g == kBV / kCols - 1) {
+        if (g == 3) {
           dev::tc_fence_before();
           __syncwarp();
           if (lane == 0) dev::mbar_arrive(dsempty);
         }
         const dev::f2 dh2 = dev::pk(dh, dh), dl2 = dev::pk(dl, dl);
 #pragma unroll
-        for (int e = 0; e < kCols; e += 2) {
-          float *x = S + kCols * g + e;
+        for (int e = 0; e < 16; e += 2) {
+          float *x = S + 16 * g + e;
           const dev::f2 old = dev::pk(x[0], x[1]);
-          const dev::f2 lo = dev::fma2(old, dl2, dev::pk(d1[e], d1[e + 1]));
-          dev::upk(dev::fma2(old, dh2, dev::add2(lo, dev::pk(d0[e], d0[e + 1]))), x[0], x[1]);
+          dev::f2 lo = dev::pk(d1[e], d1[e + 1]);
+          if (KB == 1) lo = dev::add2(lo, dev::pk(d2[e], d2[e + 1]));
+          lo = dev::add2(dev::fma2(old, dl2, lo), dev::pk(d0[e], d0[e + 1]));
+          dev::upk(dev::fma2(old, dh2, lo), x[0], x[1]);
         }
       }
       if (OUT && i + 1 < nloc) {
@@ -667,11 +706,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     dev::regs_dec<R::scale>();
-    scale_z();
+    bool ok = true;
+    for (int i = 0; i < nloc; ++i) scale_z(i, ok);
   }
   dev::tc_fence_before();
   __syncthreads();
-  if (warp == 1) dev::tmem_dealloc(tmem, kTmemCols);
+  if (warp == kIssueWarp) dev::tmem_dealloc(tmem, kTmemCols);
 }
 
 // ---------------------------------------------------------------- host
@@ -692,18 +732,26 @@ bool make_map(CUtensorMap *m, const DView &v, const DecayWalk &w, int channels) 
   return tc::map4_bf16(m, v.p, dims, strides, 64, kC);
 }
 
+template <typename Kern>
+int prepare(Kern kernel, int smem) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess ? GLA_OK
+                                                                                                       : GLA_ERR_CUDA;
+}
+
 template <int KB, bool REV>
 int launch(const DecayWalk &w, cudaStream_t st) {
   CUtensorMap mx, my, mz;
-  if (!make_map(&mx, w.x, w, w.K) || !make_map(&my, w.y, w, w.K) || !make_map(&mz, w.z, w, w.V))
-    return GLA_ERR_CUDA;
-  const int smem = Smem<KB>::bytes + 1024;
-  if (cudaFuncSetAttribute(k_decay_tc<KB, true, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-      cudaFuncSetAttribute(k_decay_tc<KB, false, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return GLA_ERR_CUDA;
+  if (!make_map(&mx, w.x, w, w.K) || !make_map(&my, w.y, w, w.K) || !make_map(&mz, w.z, w, w.V)) return GLA_ERR_CUDA;
   const unsigned gx = (unsigned)((long)w.nseq * w.H * ((w.V + kBV - 1) / kBV));
-  if (w.P > 1)
-    GLA_LAUNCH(K_DECAY_STATES, st, (k_decay_tc<KB, false, REV><<<dim3(gx, w.P - 1), kThreads, smem, st>>>(w, mx, my, mz)));
+  if (w.P > 1) {
+    // the states of 128 channels do not meet those of the others before the outputs
+    constexpr int smem = Smem<1>::bytes + 1024;
+    if (const int e = prepare(k_decay_tc<1, false, REV>, smem)) return e;
+    GLA_LAUNCH(K_DECAY_STATES, st,
+               (k_decay_tc<1, false, REV><<<dim3(gx, w.P - 1, KB), kThreads, smem, st>>>(w, mx, my, mz)));
+  }
+  constexpr int smem = Smem<KB>::bytes + 1024;
+  if (const int e = prepare(k_decay_tc<KB, true, REV>, smem)) return e;
   GLA_LAUNCH(K_DECAY_WALK, st, (k_decay_tc<KB, true, REV><<<dim3(gx, w.P), kThreads, smem, st>>>(w, mx, my, mz)));
   return GLA_OK;
 }
@@ -717,9 +765,9 @@ bool decay_tc_takes(const DecayWalk &w, int dtype) {
          ok_view(w.z, w) && ok_view(w.o, w);
 }
 
-int decay_walk_tc(const DecayWalk &w, cudaStream_t st) { 
+int decay_walk_tc(const DecayWalk &w, cudaStream_t st) {
   if (w.reverse) return w.K <= 128 ? launch<1, true>(w, st) : launch<2, true>(w, st);
   return w.K <= 128 ? launch<1, false>(w, st) : launch<2, false>(w, st);
- }
+}
 
 }  // namespace gla
