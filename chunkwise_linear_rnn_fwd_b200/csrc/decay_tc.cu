@@ -56,6 +56,14 @@ struct Regs {
   static_assert(roles + rows + (KB == 1 ? state + scale : 2 * state) <= 4 * 128, "more than the launch allocates");
 };
 
+// Sets a warpgroup's budget: the instruction that lowers a budget faults on a higher one.
+constexpr int kRegsLaunch = 65536 / kThreads;
+template <int N>
+__device__ __forceinline__ void set_regs() {
+  if constexpr (N > kRegsLaunch) dev::regs_inc<N>();
+  if constexpr (N < kRegsLaunch) dev::regs_dec<N>();
+}
+
 // KB: 128-channel blocks of the contraction
 template <int KB>
 struct Smem {
@@ -98,7 +106,8 @@ __device__ __forceinline__ void st_global_32(void *p, const uint32_t *w) {
                : "memory");
 }
 
-template <int KB, bool OUT, bool REV>
+// ACC: a contraction taken in pieces, with partial outputs read or written
+template <int KB, bool OUT, bool REV, bool ACC>
 __global__ void __launch_bounds__(kThreads, 1)
     k_decay_tc(const __grid_constant__ DecayWalk w, const __grid_constant__ CUtensorMap tmX,
                const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmZ) {
@@ -152,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int ksteps = (w.K + 15) / 16, kblocks = (w.K + 63) / 64;
   // of channel block kb: 16-channel steps, 64-column blocks
   auto ksteps_of = [&](int kb) { return min(8, ksteps - 8 * kb); };
-  auto kblocks_of = [&](int kb) { return min(2, kblocks - 2 * (kz + kb)); };
+  auto kblocks_of = [&](int kb) { return max(0, min(2, kblocks - 2 * (kz + kb))); };
   auto slot = [&](int i, int kb) { return (i * KB + kb) & 1; };
   auto phase = [&](int i, int kb) { return (uint32_t)(((i * KB + kb) >> 1) & 1); };
   auto load_y = [&](int i, int kb) {
@@ -201,33 +210,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint8_t *zt = smem + L::z + s * L::kZTile, *zw = smem + L::zw;
       // a row is eight 16-byte units; their place in the swizzled row does not matter here
       if (ok && m == kC) {
-        // units are read eight at a time, before the wait and before the first store
-#pragma unroll
-        for (int j0 = 0; j0 < kIter; j0 += 8) {
-        uint4 u[8];
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int r = (t0 + (j0 + j) * kStep) >> 3;
-          f[j] = W[REV ? r + 1 : kC - 1 - r];
-          u[j] = *reinterpret_cast<const uint4 *>(zt + 16 * (t0 + (j0 + j) * kStep));
-        }
-        if (j0 == 0 && i > 0) ok = dev::mbar_wait(dsfull, (uint32_t)((i - 1) & 1), w.status);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int e = 16 * (t0 + (j0 + j) * kStep);
+        if (i > 0) ok = dev::mbar_wait(dsfull, (uint32_t)((i - 1) & 1), w.status);
+#pragma unroll 1
+        for (int j = 0; j < kIter; j += 2) {
+          const int e = 16 * (t0 + j * kStep), r = (t0 + j * kStep) >> 3;
+          const uint4 u0 = *reinterpret_cast<const uint4 *>(zt + e), u1 = *reinterpret_cast<const uint4 *>(zt + e + 16 * kStep);
+          const float f0 = W[REV ? r + 1 : kC - 1 - r], f1 = W[REV ? r + kStep / 8 + 1 : kC - 1 - kStep / 8 - r];
           uint4 zh, zm, zl;
-          split3(u[j], f[j], zh, zm, zl);
+          split3(u0, f0, zh, zm, zl);
           *reinterpret_cast<uint4 *>(zw + e) = zh;
           *reinterpret_cast<uint4 *>(zw + L::kZTile + e) = zm;
           *reinterpret_cast<uint4 *>(zw + 2 * L::kZTile + e) = zl;
-        }
+          split3(u1, f1, zh, zm, zl);
+          *reinterpret_cast<uint4 *>(zw + e + 16 * kStep) = zh;
+          *reinterpret_cast<uint4 *>(zw + L::kZTile + e + 16 * kStep) = zm;
+          *reinterpret_cast<uint4 *>(zw + 2 * L::kZTile + e + 16 * kStep) = zl;
         }
       } else if (ok) {
-        // rows behind the sequence hold anything, and zero times it must not be NaN: those
-        // that the products read are cleared
+        // Rows behind the sequence hold anything, and zero times it must not be NaN: Y's are
+        // cleared (X Y^T of this chunk waits for it), and so are those of Z that the products read.
         const int m16 = (m + 15) & ~15;
         if (i > 0) ok = dev::mbar_wait(dsfull, (uint32_t)((i - 1) & 1), w.status);
+#pragma unroll 1
         for (int u = t0; u < m16 * 8; u += kStep) {
           const int r = u >> 3, e = 16 * u;
           uint4 zh, zm, zl, a = *reinterpret_cast<const uint4 *>(zt + e);
@@ -240,11 +244,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4 *>(zw + L::kZTile + e) = zm;
           *reinterpret_cast<uint4 *>(zw + 2 * L::kZTile + e) = zl;
         }
-        const int dead = (m16 - m) * 8;
+        const int dead = (kC - m) * 8;
         for (int kb = 0; kb < KB; ++kb) {
           const int sy = slot(i, kb);
           if (ok) ok = dev::mbar_wait(&yfull[sy], phase(i, kb), w.status);
           if (!ok) break;
+#pragma unroll 1
           for (int u = t0; u < dead * kblocks_of(kb); u += kStep)
             *reinterpret_cast<uint4 *>(smem + L::y + sy * L::kTile + (u / dead) * kC * 128 + m * 128 + (u % dead) * 16) =
                 make_uint4(0, 0, 0, 0);
@@ -263,14 +268,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   // products, whose operands take all its bandwidth.
   const float lam1 = W[1];
   const dev::f2 lam2 = dev::pk(W[2], W[2]), lam8 = dev::pk(W[8], W[8]);
-  auto mask_tail = [&](float *sc, int jb, int t, int m) {
-    // rows behind the sequence hold anything: replaced, not multiplied
-#pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const int j = 32 * jb + e;
-      sc[e] = (REV ? j >= t && j < m : j <= t) ? sc[e] : 0.f;
-    }
-  };
   auto store_p = [&](uint32_t base, const float *sc, int jb) {
     uint32_t p[16];
 #pragma unroll
@@ -291,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   // the helpers' share: two blocks away from the diagonal
   auto help_p = [&](int i, bool &ok) {
-    const int q4 = warp & 3, t = 32 * q4 + lane, m = live_of(i), jb0 = REV ? 2 : 0;
+    const int q4 = warp & 3, t = 32 * q4 + lane, jb0 = REV ? 2 : 0;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * q4) << 16);
     if (ok) ok = dev::mbar_wait(scfull, (uint32_t)(i & 1), w.status);
     dev::tc_fence_after();
@@ -302,7 +299,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float near = W[REV ? 32 * (jb0 + u) - t : t - 32 * (jb0 + u) - 31];
       dev::tmem_wait_ld();
       weigh(sc, near);
-      if (m < kC) mask_tail(sc, jb0 + u, t, m);
       store_p(lane_base, sc, jb0 + u);
     }
     dev::tmem_wait_st();
@@ -312,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp < 4) {
-    dev::regs_dec<R::roles>();
+    set_regs<R::roles>();
     if (warp == kLoadWarp) {
     // ============================ loads ============================
     if (lane == 0 && nloc > 0) {
@@ -370,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     // X Y^T of chunk i
     auto scores = [&](int i) {
+      if (live_of(i) < kC) ok = ok && wait(zready, (uint32_t)(i & 1));  // Y's rows behind the sequence are cleared
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
         const int s = slot(i, kb);
@@ -475,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 8) {
     // ============================ P and O ============================
-    dev::regs_inc<R::rows>();
+    set_regs<R::rows>();
     if (OUT) {
       const int q4 = warp & 3, t = 32 * q4 + lane;
       const uint32_t lane_base = tmem + ((uint32_t)(32 * q4) << 16);
@@ -505,13 +502,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 32; e += 2)
           dev::upk(dev::mul2(dev::pk(sc[e], sc[e + 1]), dev::pk(fd[e], fd[e + 1])), sc[e], sc[e + 1]);
-        if (m < kC) mask_tail(sc, q4, t, m);
         store_p(lane_base, sc, q4);
         if (beside) {
           dev::tmem_ld32(lane_base + kColSc + 32 * jo, sc);
           dev::tmem_wait_ld();
           weigh(sc, near);
-          if (m < kC) mask_tail(sc, jo, t, m);
           store_p(lane_base, sc, jo);
         } else {
           const uint32_t zero[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
@@ -532,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float f = W[t < m ? (REV ? m - 1 - t : t + 1) : 0];
         __nv_bfloat16 *o = (__nv_bfloat16 *)w.o.p + sq.b * w.o.sb + h * w.o.sh + (row0 + t) * w.o.st + v0;
         const bool live = t < m && ok;
-#pragma unroll
+#pragma unroll 1
         for (int hf = 0; hf < 2; ++hf) {
           float a[32], c[32];
           dev::tmem_ld32(lane_base + kColOa + 32 * hf, a);
@@ -547,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; e += 2)
             dev::upk(dev::fma2(f2v, dev::pk(c[e], c[e + 1]), dev::pk(a[e], a[e + 1])), a[e], a[e + 1]);
-          if (live && (w.acc_in || w.acc_out)) {
+          if (ACC && live) {
             const long row = w.packed ? row0 + t : (long)b * w.T + row0 + t;
             float *part = w.acc + ((long)h * rows + row) * w.V + v0 + 32 * hf;
 #pragma unroll
@@ -565,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t r[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) r[e] = dev::pack_bf16(a[2 * e], a[2 * e + 1]);
-          if (!live || w.acc_out) continue;
+          if (!live || (ACC && w.acc_out)) continue;
           if (wide && nv == kBV) {
             st_global_32(o + 32 * hf, r);
             st_global_32(o + 32 * hf + 16, r + 8);
@@ -581,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 8 + kStateWarps) {
     // ============================ state ============================
-    if (KB == 1) dev::regs_inc<R::state>();
+    set_regs<R::state>();
     const int q4 = warp & 3, kb = (warp - 8) >> 2, kc = 128 * kb + 32 * q4 + lane, kr = 128 * kz + kc;  // this thread's channel (of the CTA's, of all)
     const uint32_t lane_base = tmem + ((uint32_t)(32 * q4) << 16);
     const long KV = (long)w.K * w.V;
@@ -705,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    dev::regs_dec<R::scale>();
+    set_regs<R::scale>();
     bool ok = true;
     for (int i = 0; i < nloc; ++i) scale_z(i, ok);
   }
@@ -738,7 +733,7 @@ int prepare(Kern kernel, int smem) {
                                                                                                        : GLA_ERR_CUDA;
 }
 
-template <int KB, bool REV>
+template <int KB, bool REV, bool ACC>
 int launch(const DecayWalk &w, cudaStream_t st) {
   CUtensorMap mx, my, mz;
   if (!make_map(&mx, w.x, w, w.K) || !make_map(&my, w.y, w, w.K) || !make_map(&mz, w.z, w, w.V)) return GLA_ERR_CUDA;
@@ -746,13 +741,13 @@ int launch(const DecayWalk &w, cudaStream_t st) {
   if (w.P > 1) {
     // the states of 128 channels do not meet those of the others before the outputs
     constexpr int smem = Smem<1>::bytes + 1024;
-    if (const int e = prepare(k_decay_tc<1, false, REV>, smem)) return e;
+    if (const int e = prepare(k_decay_tc<1, false, REV, false>, smem)) return e;
     GLA_LAUNCH(K_DECAY_STATES, st,
-               (k_decay_tc<1, false, REV><<<dim3(gx, w.P - 1, KB), kThreads, smem, st>>>(w, mx, my, mz)));
+               (k_decay_tc<1, false, REV, false><<<dim3(gx, w.P - 1, w.K > 128 ? 2 : 1), kThreads, smem, st>>>(w, mx, my, mz)));
   }
   constexpr int smem = Smem<KB>::bytes + 1024;
-  if (const int e = prepare(k_decay_tc<KB, true, REV>, smem)) return e;
-  GLA_LAUNCH(K_DECAY_WALK, st, (k_decay_tc<KB, true, REV><<<dim3(gx, w.P), kThreads, smem, st>>>(w, mx, my, mz)));
+  if (const int e = prepare(k_decay_tc<KB, true, REV, ACC>, smem)) return e;
+  GLA_LAUNCH(K_DECAY_WALK, st, (k_decay_tc<KB, true, REV, ACC><<<dim3(gx, w.P), kThreads, smem, st>>>(w, mx, my, mz)));
   return GLA_OK;
 }
 
@@ -766,8 +761,9 @@ bool decay_tc_takes(const DecayWalk &w, int dtype) {
 }
 
 int decay_walk_tc(const DecayWalk &w, cudaStream_t st) {
-  if (w.reverse) return w.K <= 128 ? launch<1, true>(w, st) : launch<2, true>(w, st);
-  return w.K <= 128 ? launch<1, false>(w, st) : launch<2, false>(w, st);
+  if (w.acc_in || w.acc_out) return w.reverse ? launch<2, true, true>(w, st) : launch<2, false, true>(w, st);
+  if (w.reverse) return w.K <= 128 ? launch<1, true, false>(w, st) : launch<2, true, false>(w, st);
+  return w.K <= 128 ? launch<1, false, false>(w, st) : launch<2, false, false>(w, st);
 }
 
 }  // namespace gla
