@@ -277,9 +277,15 @@ __global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
 template <typename T, int C, int K>
 int launch_cc(const DecayWalk &w, cudaStream_t st) {
   const int smem = CcSmem<C, K>::floats * 4;
-  if (cudaFuncSetAttribute(k_decay_cc<T, C, K, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-      cudaFuncSetAttribute(k_decay_cc<T, C, K, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return GLA_ERR_CUDA;
+  static DeviceSlots slots;  // the kernels' shared memory is set once per device
+  const int ready = per_device(slots, [smem] {
+    cudaError_t e = cudaFuncSetAttribute(k_decay_cc<T, C, K, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k_decay_cc<T, C, K, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) note_cuda_error(e);
+    return e == cudaSuccess ? 1 : -1;
+  });
+  if (ready != 1) return GLA_ERR_CUDA;
   const unsigned gx = (unsigned)((long)w.nseq * w.H * ((w.V + kBV - 1) / kBV));
   if (w.P > 1)
     GLA_LAUNCH(K_DECAY_STATES, st, (k_decay_cc<T, C, K, false><<<dim3(gx, w.P - 1), kThreads, smem, st>>>(w)));
@@ -297,14 +303,15 @@ int walk_cc(const DecayWalk &w, cudaStream_t st) {
 // ============================================================================
 // The recurrent step: one token per sequence.  Reads and rewrites the state once
 // (2 * 4 * dk * dv bytes a head) and is bound by HBM on it, or by latency where the batch
-// is small.  CTA = (kStepCols columns, sequence and head); a thread owns four columns and
-// every RG-th row, all of whose loads are issued before the first is used; the sums over
-// the rows go through shared memory.
+// is small.  CTA = (4 CQ columns, sequence and head); a thread owns four columns and every
+// RG-th row, kBatch of them loaded together, the first ones before anything else (a store
+// between two loads of the state would hold the second back); the sums over the rows go
+// through shared memory.
 // ============================================================================
 template <typename T, int CQ>  // CQ: quads of columns per CTA
 __global__ void __launch_bounds__(256) k_decay_step(int H, int nseq, int K, int V, DView q, DView k, DView v, DView o,
                                                     const float *ld, DPool s, unsigned *status) {
-  constexpr int RG = 256 / CQ;
+  constexpr int RG = 256 / CQ, kBatch = 8;
   __shared__ float sq[256], sk[256];
   __shared__ float4 red[RG][CQ];
   const int tid = threadIdx.x, jq = tid % CQ, rg = tid / CQ;
@@ -316,45 +323,65 @@ __global__ void __launch_bounds__(256) k_decay_step(int H, int nseq, int K, int 
   const DPool none{};
   dev::decay_slots(none, s, false, nseq, b, status, i0, i1);
   if (i1 < 0) return;
+  const int col = vt * 4 * CQ + 4 * jq;
+  float *S = s.p + i1 * s.slot + h * s.head + col;
+  const bool quads = V % 4 == 0;  // the pool is 16-byte aligned
+  const int nv = min(4, V - col);
+  auto load = [&](int r) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < K) {
+      const float *p = S + (long)r * V;
+      if (quads) {
+        if (nv > 0) x = *reinterpret_cast<const float4 *>(p);
+      } else {
+        if (nv > 0) x.x = p[0];
+        if (nv > 1) x.y = p[1];
+        if (nv > 2) x.z = p[2];
+        if (nv > 3) x.w = p[3];
+      }
+    }
+    return x;
+  };
+  float4 x[kBatch];
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j) x[j] = load(rg + j * RG);
   const float lam = (float)dev::decay_pow(dev::decay_rate(ld, h, status), 1);
   if (tid < K) {
     sq[tid] = to_f(((const T *)q.p)[b * q.sb + h * q.sh + tid]);
     sk[tid] = to_f(((const T *)k.p)[b * k.sb + h * k.sh + tid]);
   }
-  __syncthreads();
-  const int col = vt * 4 * CQ + 4 * jq;
   const T *vp = (const T *)v.p + b * v.sb + h * v.sh + col;
-  float *S = s.p + i1 * s.slot + h * s.head + col;
   float vv[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) vv[e] = col + e < V ? to_f(vp[e]) : 0.f;
-  if (V % 4 == 0) {
-    if (col < V)
-#pragma unroll 8
-      for (int r = rg; r < K; r += RG) {
-        float4 *p = reinterpret_cast<float4 *>(S + (long)r * V);
-        float4 x = *p;
-        const float kr = sk[r], qr = sq[r];
-        x.x = fmaf(lam, x.x, kr * vv[0]);
-        x.y = fmaf(lam, x.y, kr * vv[1]);
-        x.z = fmaf(lam, x.z, kr * vv[2]);
-        x.w = fmaf(lam, x.w, kr * vv[3]);
-        *p = x;
-        acc[0] = fmaf(qr, x.x, acc[0]);
-        acc[1] = fmaf(qr, x.y, acc[1]);
-        acc[2] = fmaf(qr, x.z, acc[2]);
-        acc[3] = fmaf(qr, x.w, acc[3]);
-      }
-  } else {
-    for (int r = rg; r < K; r += RG)
+  for (int e = 0; e < 4; ++e) vv[e] = e < nv ? to_f(vp[e]) : 0.f;
+  __syncthreads();
+  for (int r0 = rg;; r0 += RG * kBatch) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (col + e < V) {
-          float *p = S + (long)r * V + e;
-          const float x = fmaf(lam, *p, sk[r] * vv[e]);
-          *p = x;
-          acc[e] = fmaf(sq[r], x, acc[e]);
-        }
+    for (int j = 0; j < kBatch; ++j) {
+      const int r = r0 + j * RG;
+      if (r >= K) continue;
+      const float kr = sk[r], qr = sq[r];
+      x[j].x = fmaf(lam, x[j].x, kr * vv[0]);
+      x[j].y = fmaf(lam, x[j].y, kr * vv[1]);
+      x[j].z = fmaf(lam, x[j].z, kr * vv[2]);
+      x[j].w = fmaf(lam, x[j].w, kr * vv[3]);
+      acc[0] = fmaf(qr, x[j].x, acc[0]);
+      acc[1] = fmaf(qr, x[j].y, acc[1]);
+      acc[2] = fmaf(qr, x[j].z, acc[2]);
+      acc[3] = fmaf(qr, x[j].w, acc[3]);
+      float *p = S + (long)r * V;
+      if (quads) {
+        if (nv > 0) *reinterpret_cast<float4 *>(p) = x[j];
+      } else {
+        if (nv > 0) p[0] = x[j].x;
+        if (nv > 1) p[1] = x[j].y;
+        if (nv > 2) p[2] = x[j].z;
+        if (nv > 3) p[3] = x[j].w;
+      }
+    }
+    if (r0 + RG * kBatch - rg >= K) break;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) x[j] = load(r0 + (kBatch + j) * RG);
   }
   red[rg][jq] = make_float4(acc[0], acc[1], acc[2], acc[3]);
   __syncthreads();
@@ -362,11 +389,29 @@ __global__ void __launch_bounds__(256) k_decay_step(int H, int nseq, int K, int 
     const int c = vt * 4 * CQ + tid;
     if (c < V) {
       float sum = 0.f;
-#pragma unroll
+#pragma unroll 8
       for (int g = 0; g < RG; ++g) sum += (&red[g][tid / 4].x)[tid % 4];
       ((T *)o.p)[b * o.sb + h * o.sh + c] = from_f<T>(sum);
     }
   }
+}
+
+template <typename T, int CQ>
+int launch_step(const gla_decay_desc &d, const DView &q, const DView &k, const DView &v, const DView &o, const float *ld,
+                const DPool &s, cudaStream_t st) {
+  const long grid = (long)d.B * d.H * ((d.dv + 4 * CQ - 1) / (4 * CQ));
+  GLA_LAUNCH(K_DECAY_STEP, st,
+             (k_decay_step<T, CQ><<<(unsigned)grid, 256, 0, st>>>(d.H, d.B, d.dk, d.dv, q, k, v, o, ld, s,
+                                                                  (unsigned *)d.workspace)));
+  return GLA_OK;
+}
+
+// 64 columns a CTA, or 16 where those would leave SMs idle
+template <typename T>
+int step(const gla_decay_desc &d, const DView &q, const DView &k, const DView &v, const DView &o, const float *ld,
+         const DPool &s, cudaStream_t st) {
+  if ((long)d.B * d.H * ((d.dv + 63) / 64) >= 2 * 148) return launch_step<T, 16>(d, q, k, v, o, ld, s, st);
+  return launch_step<T, 4>(d, q, k, v, o, ld, s, st);
 }
 
 }  // namespace
@@ -591,18 +636,8 @@ int gla_decay_step(const gla_decay_desc *desc, const gla_view *q, const gla_view
   GLA_TRY(check_view(o, d.dtype, &vo));
   const DPool s = pool(state, index, d.slots1, &d, false);
   cudaStream_t st = (cudaStream_t)stream;
-  unsigned *status = (unsigned *)d.workspace;
-  constexpr int CQ = 16;
-  const long grid = (long)d.B * d.H * ((d.dv + 4 * CQ - 1) / (4 * CQ));
-  if (d.dtype == GLA_DTYPE_BF16)
-    GLA_LAUNCH(K_DECAY_STEP, st,
-               (k_decay_step<__nv_bfloat16, CQ><<<(unsigned)grid, 256, 0, st>>>(d.H, d.B, d.dk, d.dv, vq, vk, vv, vo,
-                                                                                log_decay, s, status)));
-  else
-    GLA_LAUNCH(K_DECAY_STEP, st,
-               (k_decay_step<float, CQ><<<(unsigned)grid, 256, 0, st>>>(d.H, d.B, d.dk, d.dv, vq, vk, vv, vo,
-                                                                        log_decay, s, status)));
-  return GLA_OK;
+  return d.dtype == GLA_DTYPE_BF16 ? step<__nv_bfloat16>(d, vq, vk, vv, vo, log_decay, s, st)
+                                   : step<float>(d, vq, vk, vv, vo, log_decay, s, st);
 }
 
 }  // extern "C"

@@ -727,10 +727,16 @@ bool make_map(CUtensorMap *m, const DView &v, const DecayWalk &w, int channels) 
   return tc::map4_bf16(m, v.p, dims, strides, 64, kC);
 }
 
-template <typename Kern>
-int prepare(Kern kernel, int smem) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess ? GLA_OK
-                                                                                                       : GLA_ERR_CUDA;
+// A kernel's shared memory, set once per device.
+template <auto kernel>
+int prepare(int smem) {
+  static DeviceSlots slots;
+  const int e = per_device(slots, [smem] {
+    const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (r != cudaSuccess) note_cuda_error(r);
+    return r == cudaSuccess ? 1 : -1;
+  });
+  return e == 1 ? GLA_OK : GLA_ERR_CUDA;
 }
 
 template <int KB, bool REV, bool ACC>
@@ -741,12 +747,12 @@ int launch(const DecayWalk &w, cudaStream_t st) {
   if (w.P > 1) {
     // the states of 128 channels do not meet those of the others before the outputs
     constexpr int smem = Smem<1>::bytes + 1024;
-    if (const int e = prepare(k_decay_tc<1, false, REV, false>, smem)) return e;
+    if (const int e = prepare<k_decay_tc<1, false, REV, false>>(smem)) return e;
     GLA_LAUNCH(K_DECAY_STATES, st,
                (k_decay_tc<1, false, REV, false><<<dim3(gx, w.P - 1, w.K > 128 ? 2 : 1), kThreads, smem, st>>>(w, mx, my, mz)));
   }
   constexpr int smem = Smem<KB>::bytes + 1024;
-  if (const int e = prepare(k_decay_tc<KB, true, REV, ACC>, smem)) return e;
+  if (const int e = prepare<k_decay_tc<KB, true, REV, ACC>>(smem)) return e;
   GLA_LAUNCH(K_DECAY_WALK, st, (k_decay_tc<KB, true, REV, ACC><<<dim3(gx, w.P), kThreads, smem, st>>>(w, mx, my, mz)));
   return GLA_OK;
 }

@@ -177,87 +177,150 @@ __global__ void __launch_bounds__(G < kLnThreads ? kLnThreads : G) k_ln_fwd(LnAr
   }
 }
 
-// The whole CTA of G threads takes one row after another; thread t owns the columns
-// VEC (t + G i) .. in every row and carries their sums of dy x^ and dy.
-template <typename T, int VEC, int N, int G>
-__global__ void __launch_bounds__(G) k_ln_bwd(LnArgs a) {
-  __shared__ float2 red[2][32];
-  const int t = threadIdx.x, warp = t >> 5;
+// A group of G threads (a warp, or the whole CTA for wide rows) takes R rows at a time;
+// thread t of it owns the columns VEC (t + G i) .. in every row and carries their sums of
+// dy x^ and dy.  The next rows' loads are issued before these are worked on.
+template <typename T, int VEC, int N, int G, int R>
+__global__ void __launch_bounds__(G < kLnThreads ? kLnThreads : G, G <= kLnThreads ? 2 : 1) k_ln_bwd(LnArgs a) {
+  constexpr int kGroups = G < kLnThreads ? kLnThreads / G : 1;
+  __shared__ float2 red[2][R][32];
+  extern __shared__ float sums[];  // [groups][2][d], with more than one group
+  const int t = threadIdx.x % G, warp = threadIdx.x >> 5, group = threadIdx.x / G;
   const float inv = 1.f / (float)a.d;
+  const long step = (long)gridDim.x * kGroups * R;
   float dw[N * VEC], db[N * VEC];
 #pragma unroll
   for (int i = 0; i < N * VEC; ++i) dw[i] = db[i] = 0.f;
-  int par = 0;
-  for (long row = blockIdx.x; row < a.rows; row += gridDim.x, par ^= 1) {
-    const T *x = (const T *)a.x + row * a.ldx, *dy = (const T *)a.dy + row * a.lddy;
-    Pack<T, VEC> px[N], pg[N];
+  // wide rows (many values a thread) keep neither the weights nor the next rows
+  constexpr bool kKeep = N * VEC <= 16;
+  struct Rows {
+    Pack<T, VEC> x[R][N], g[R][N];
+    float mean[R], rstd[R];
+  };
+  auto load = [&](Rows &p, long row0) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = VEC * (t + G * i);
-      if (c < a.d) px[i].load(x + c), pg[i].load(dy + c);
+    for (int r = 0; r < R; ++r) {
+      const long row = row0 + r;
+      p.mean[r] = p.rstd[r] = 0.f;
+      if (row < a.rows) {
+        const T *x = (const T *)a.x + row * a.ldx, *dy = (const T *)a.dy + row * a.lddy;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int c = VEC * (t + G * i);
+          if (c < a.d) p.x[r][i].load(x + c), p.g[r][i].load(dy + c);
+        }
+        p.mean[r] = __ldg(a.cmean + row);
+        p.rstd[r] = __ldg(a.crstd + row);
+      }
     }
-    const float mean = __ldg(a.cmean + row), rstd = __ldg(a.crstd + row);
-    float s1 = 0.f, s2 = 0.f;
+  };
+  float kept[kKeep ? N * VEC : 1];
+  auto weights = [&](int i, float *w) {
+    const int c = VEC * (t + G * i);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) w[e] = 1.f;
+    if (c < a.d && a.w) ldv<VEC>(a.w + c, w);
+  };
+  if constexpr (kKeep)
+#pragma unroll
+    for (int i = 0; i < N; ++i) weights(i, kept + i * VEC);
+  int par = 0;
+  long row0 = ((long)blockIdx.x * kGroups + group) * R;
+  Rows p;
+  load(p, row0);
+  // (G > 32: one group a CTA, so that every thread makes the same number of rounds)
+  for (; row0 < a.rows; row0 += step, par ^= 1) {
+    Rows next;
+    if constexpr (kKeep) load(next, row0 + step);
+    float s1[R], s2[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) s1[r] = s2[r] = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = VEC * (t + G * i);
-      if (c < a.d) {
-        float xv[VEC], gv[VEC], w[VEC];
-        px[i].get(xv);
-        pg[i].get(gv);
+      float w[VEC];
+      if constexpr (!kKeep) weights(i, w);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) w[e] = 1.f;
-        if (a.w) ldv<VEC>(a.w + c, w);
+      for (int r = 0; r < R; ++r) {
+        if (c < a.d && row0 + r < a.rows) {
+          float xv[VEC], gv[VEC];
+          p.x[r][i].get(xv);
+          p.g[r][i].get(gv);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float xh = (xv[e] - mean) * rstd, g = gv[e] * w[e];
-          dw[i * VEC + e] = fmaf(gv[e], xh, dw[i * VEC + e]);
-          db[i * VEC + e] += gv[e];
-          s1 += g;
-          s2 = fmaf(g, xh, s2);
+          for (int e = 0; e < VEC; ++e) {
+            const float h = (xv[e] - p.mean[r]) * p.rstd[r], g = gv[e] * (kKeep ? kept[kKeep ? i * VEC + e : 0] : w[e]);
+            dw[i * VEC + e] = fmaf(gv[e], h, dw[i * VEC + e]);
+            db[i * VEC + e] += gv[e];
+            s1[r] += g;
+            s2[r] = fmaf(g, h, s2[r]);
+          }
         }
       }
     }
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
-    if constexpr (G > 32) {
-      // two buffers in turn: a thread past the barrier of row r cannot reach row r + 2's
-      // writes before every thread has passed row r + 1's barrier
-      if ((t & 31) == 0) red[par][warp] = make_float2(s1, s2);
-      __syncthreads();
-      s1 = s2 = 0.f;
 #pragma unroll
-      for (int i = 0; i < G / 32; ++i) s1 += red[par][i].x, s2 += red[par][i].y;
+    for (int r = 0; r < R; ++r) {
+      s1[r] = warp_sum(s1[r]);
+      s2[r] = warp_sum(s2[r]);
     }
-    s1 *= inv;
-    s2 *= inv;
-    T *dx = (T *)a.out + row * a.ldo;
+    if constexpr (G > 32) {
+      // two buffers in turn: a thread past the barrier of one round cannot reach the writes
+      // of the round after the next before every thread has passed the next one's barrier
+      if ((t & 31) == 0)
+#pragma unroll
+        for (int r = 0; r < R; ++r) red[par][r][warp] = make_float2(s1[r], s2[r]);
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        s1[r] = s2[r] = 0.f;
+#pragma unroll
+        for (int i = 0; i < G / 32; ++i) s1[r] += red[par][r][i].x, s2[r] += red[par][r][i].y;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = VEC * (t + G * i);
-      if (c < a.d) {
-        float xv[VEC], gv[VEC], w[VEC];
-        px[i].get(xv);
-        pg[i].get(gv);
+      float w[VEC];
+      if constexpr (!kKeep) weights(i, w);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) w[e] = 1.f;
-        if (a.w) ldv<VEC>(a.w + c, w);
+      for (int r = 0; r < R; ++r) {
+        if (c < a.d && row0 + r < a.rows) {
+          const float m1 = s1[r] * inv, m2 = s2[r] * inv;
+          float xv[VEC], gv[VEC];
+          p.x[r][i].get(xv);
+          p.g[r][i].get(gv);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) xv[e] = rstd * (gv[e] * w[e] - s1 - (xv[e] - mean) * rstd * s2);
-        px[i].put(xv);
-        px[i].store(dx + c);
+          for (int e = 0; e < VEC; ++e) {
+            const float h = (xv[e] - p.mean[r]) * p.rstd[r], g = gv[e] * (kKeep ? kept[kKeep ? i * VEC + e : 0] : w[e]);
+            xv[e] = p.rstd[r] * (g - m1 - h * m2);
+          }
+          Pack<T, VEC> out;
+          out.put(xv);
+          out.store((T *)a.out + (row0 + r) * a.ldo + c);
+        }
       }
     }
+    if constexpr (kKeep) p = next;
+    else load(p, row0 + step);
   }
   if (!a.part) return;
   float *part = a.part + (long)blockIdx.x * 2 * a.d;
+  float *mine = kGroups > 1 ? sums + (long)group * 2 * a.d : part;
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const int c = VEC * (t + G * i) + e;
-      if (c < a.d) part[c] = dw[i * VEC + e], part[a.d + c] = db[i * VEC + e];
+      if (c < a.d) mine[c] = dw[i * VEC + e], mine[a.d + c] = db[i * VEC + e];
     }
+  if constexpr (kGroups > 1) {  // the CTA's groups in order
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * a.d; c += kLnThreads) {
+      float s = 0.f;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) s += sums[(long)g * 2 * a.d + c];
+      part[c] = s;
+    }
+  }
 }
 
 // dw, db from the partial sums: a CTA owns 32 of the 2 d columns, warp v adds the partials
@@ -297,32 +360,42 @@ int fwd_launch(const LnArgs &a, cudaStream_t st) {
   return GLA_OK;
 }
 
-template <typename T, int VEC, int N, int G>
+template <typename T, int VEC, int N, int G, int R>
 int bwd_launch(const LnArgs &a, float *dw, float *db, cudaStream_t st) {
-  const long grid = bwd_ctas(a.rows);
-  GLA_LAUNCH(K_LN_BWD, st, (k_ln_bwd<T, VEC, N, G><<<(unsigned)grid, G, 0, st>>>(a)));
+  constexpr int kGroups = G < kLnThreads ? kLnThreads / G : 1;
+  const long rounds = (a.rows + kGroups * R - 1) / (kGroups * R), most = bwd_ctas(a.rows);
+  const long grid = rounds < most ? rounds : most;
+  const size_t smem = kGroups > 1 && a.part ? (size_t)kGroups * 2 * a.d * sizeof(float) : 0;
+  GLA_LAUNCH(K_LN_BWD, st, (k_ln_bwd<T, VEC, N, G, R><<<(unsigned)grid, G < kLnThreads ? kLnThreads : G, smem, st>>>(a)));
   if (a.part)
     GLA_LAUNCH(K_LN_REDUCE, st, (k_ln_reduce<<<(2 * a.d + 31) / 32, 1024, 0, st>>>((int)grid, a.d, a.part, dw, db)));
   return GLA_OK;
 }
 
+// Rows up to 2048 values wide (512 single ones) to a warp each, wider ones to a CTA.
 template <typename T, int VEC>
 int fwd_t(const LnArgs &a, cudaStream_t st) {
   const int n = (a.d + VEC - 1) / VEC;  // packs of a row
   constexpr int F = VEC == 1 ? 4 : VEC == 4 ? 2 : 1;  // packs per thread that make 8 values, or 4 single ones
   if (n <= 32 * F) return fwd_launch<T, VEC, F, 32>(a, st);
   if (n <= 32 * 4 * F) return fwd_launch<T, VEC, 4 * F, 32>(a, st);
+  if constexpr (VEC > 1)
+    if (n <= 32 * 8 * F) return fwd_launch<T, VEC, 8 * F, 32>(a, st);
   if (n <= 256 * 2 * F) return fwd_launch<T, VEC, 2 * F, 256>(a, st);
   return fwd_launch<T, VEC, 4 * F, VEC == 1 ? 1024 : 512>(a, st);
 }
+// Rows up to 512 values (128 single ones) to a warp each.  Four rows at a time keep 64 KB in
+// flight on an SM; wide rows do with fewer.
 template <typename T, int VEC>
 int bwd_t(const LnArgs &a, float *dw, float *db, cudaStream_t st) {
   const int n = (a.d + VEC - 1) / VEC;
   constexpr int F = VEC == 1 ? 4 : VEC == 4 ? 2 : 1;
-  if (n <= 64 * F) return bwd_launch<T, VEC, F, 64>(a, dw, db, st);
-  if (n <= 256 * F) return bwd_launch<T, VEC, F, 256>(a, dw, db, st);
-  if (n <= 512 * 2 * F) return bwd_launch<T, VEC, 2 * F, 512>(a, dw, db, st);
-  return bwd_launch<T, VEC, VEC == 1 ? 4 * F : 2 * F, 1024>(a, dw, db, st);
+  if (n <= 32 * F) return bwd_launch<T, VEC, F, 32, 4>(a, dw, db, st);
+  if constexpr (VEC > 1)
+    if (n <= 64 * F) return bwd_launch<T, VEC, 2 * F, 32, 2>(a, dw, db, st);
+  if (n <= 256 * F) return bwd_launch<T, VEC, F, 256, 4>(a, dw, db, st);
+  if (n <= 512 * 2 * F) return bwd_launch<T, VEC, 2 * F, 512, 1>(a, dw, db, st);
+  return bwd_launch<T, VEC, VEC == 1 ? 8 * F : 4 * F, 512, 1>(a, dw, db, st);
 }
 
 bool al16(const void *p) { return ((uintptr_t)p & 15u) == 0; }

@@ -114,7 +114,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gla_fwd_general.restype = i
     lib.gla_bwd_general.argtypes = [dp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, vp]
     lib.gla_bwd_general.restype = i
-    dd, vw, ll = ctypes.POINTER(gla_decay_desc), ctypes.POINTER(gla_view), ctypes.c_longlong
+    dd, vw, ll = ctypes.POINTER(gla_decay_desc), vp, ctypes.c_longlong  # vw: a gla_view's address
     lib.gla_decay_workspace_size.argtypes = [dd, i]
     lib.gla_decay_workspace_size.restype = ctypes.c_size_t
     lib.gla_decay_fwd.argtypes = [dd, vw, vw, vw, vp, vp, vp, vp, vw, vp, vp, vp]
@@ -548,50 +548,62 @@ def _on_device(fn):
 
     @functools.wraps(fn)
     def wrapper(x, *args, **kwargs):
-        if not x.is_cuda:
+        index = x.get_device()
+        if index < 0:
             raise ValueError("tensors passed to the GLA library must be on a CUDA device")
         stream = kwargs.get("stream")
+        if stream is None and index == torch._C._cuda_getDevice():
+            return fn(x, *args, **kwargs)
         if stream is not None and stream.device != x.device:
             raise ValueError("stream and tensors are on different devices")
-        if x.device.index == torch.cuda.current_device():
-            return (fn if stream is None else on_stream)(x, *args, **kwargs)
-        with torch.cuda.device(x.device):
+        with torch.cuda.device(index):
             return on_stream(x, *args, **kwargs)
     return wrapper
 
 
-def _like(t, name, dtype, shape, device):
+def _raw_stream(stream, index) -> int:
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _check(t, name, dtype, shape, index):
     """Refuse a tensor of another type, shape or device than the call needs."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device:
-        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} "
+    if t.dtype != dtype or t.shape != shape or t.get_device() != index:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on cuda:{index}, got {t.dtype} {tuple(t.shape)} "
                          f"on {t.device}")
 
 
-def _dense_ptr(t, name, dtype, shape, device):
+def _dense(t, name, dtype, shape, index):
+    """Address of a contiguous tensor, None for None."""
     if t is None:
         return None
-    _like(t, name, dtype, shape, device)
+    _check(t, name, dtype, shape, index)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _view(t, name, dtype, shape, device):
-    """gla_view of [B,H,T,d] (or [B,H,d]: one token) with contiguous channels."""
-    _like(t, name, dtype, shape, device)
-    s = t.stride()
-    if s[-1] != 1 and shape[-1] != 1:
-        raise ValueError(f"{name}: the channels of a token must be contiguous")
-    return ctypes.byref(gla_view(t.data_ptr(), s[0], s[1], s[2] if len(s) == 4 else 0))
+def _views(dtype, index, *tensors):
+    """gla_view of each (tensor [B,H,T,d] or, one token, [B,H,d], its name, its shape): an array of
+    them, and the address of the first (they lie 32 bytes apart)."""
+    v = []
+    for t, name, shape in tensors:
+        _check(t, name, dtype, shape, index)
+        s = t.stride()
+        if s[-1] != 1 and shape[-1] != 1:
+            raise ValueError(f"{name}: the channels of a token must be contiguous")
+        v += (t.data_ptr(), s[0], s[1], s[2] if len(s) == 4 else 0)
+    a = (ctypes.c_longlong * len(v))(*v)
+    return a, ctypes.addressof(a)
 
 
 def _decay_desc(B, H, T, max_len, dk, dv, dtype, slots0=0, slots1=0, segments=0, workspace=None) -> gla_decay_desc:
-    if dtype not in DTYPE:
+    code = DTYPE.get(dtype)
+    if code is None:
         raise ValueError(f"unsupported dtype {dtype}")
-    d = gla_decay_desc(B, H, T, max_len, dk, dv, DTYPE[dtype], slots0, slots1, segments, None, 0)
-    if workspace is not None:
-        d.workspace, d.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    return d
+    if workspace is None:
+        return gla_decay_desc(B, H, T, max_len, dk, dv, code, slots0, slots1, segments, None, 0)
+    return gla_decay_desc(B, H, T, max_len, dk, dv, code, slots0, slots1, segments, workspace.data_ptr(),
+                          workspace.nbytes)
 
 
 def decay_workspace_size(B, H, T, dk, dv, dtype, for_bwd=False, *, max_len=0, segments=0) -> int:
@@ -611,8 +623,8 @@ def alloc_decay_workspace(nbytes: int, device) -> torch.Tensor:
     return ws
 
 
-def _decay_setup(q, v, cu_seqlens, max_len, segments, workspace, for_bwd):
-    """(B sequences, max_len, cu pointer, workspace) of a chunked call.  A workspace the
+def _decay_setup(lib, q, v, index, cu_seqlens, max_len, slots0, slots1, segments, workspace, for_bwd):
+    """(B sequences, cu pointer, descriptor, workspace) of a chunked call.  A workspace the
     caller did not pass lives for this call; nobody reads its status word."""
     B, H, T, dk = q.shape
     if cu_seqlens is None:
@@ -625,12 +637,15 @@ def _decay_setup(q, v, cu_seqlens, max_len, segments, workspace, for_bwd):
         if max_len is None:
             raise ValueError("packed tensors need max_len, a bound on the longest sequence")
         B = cu_seqlens.numel() - 1
-        cu = _dense_ptr(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), q.device)
+        cu = _dense(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), index)
+    d = _decay_desc(B, H, T, max_len, dk, v.shape[-1], q.dtype, B if slots0 is None else slots0,
+                    B if slots1 is None else slots1, segments, workspace)
     if workspace is None:
-        workspace = torch.empty(decay_workspace_size(B, H, T, dk, v.shape[-1], q.dtype, for_bwd,
-                                                     max_len=max_len, segments=segments),
-                                dtype=torch.uint8, device=q.device)
-    return B, int(max_len), cu, workspace
+        # an invalid descriptor needs 0 bytes and is refused by the call
+        n = max(lib.gla_decay_workspace_size(ctypes.byref(d), for_bwd), 256)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        d.workspace, d.workspace_bytes = workspace.data_ptr(), n
+    return B, cu, d, workspace
 
 
 @_on_device
@@ -649,23 +664,21 @@ def gla_decay_fwd(q, k, v, log_decay, *, cu_seqlens=None, max_len=None, h0=None,
     lib = load()
     B, H, T, dk = q.shape
     dv = v.shape[-1]
-    dev, dt = q.device, q.dtype
+    index, dt, f32, i32 = q.get_device(), q.dtype, torch.float32, torch.int32
     if o is None:
-        o = torch.empty(B, H, T, dv, dtype=dt, device=dev)
-    n, max_len, cu, workspace = _decay_setup(q, v, cu_seqlens, max_len, segments, workspace, False)
-    f32, i32 = torch.float32, torch.int32
+        o = torch.empty(B, H, T, dv, dtype=dt, device=q.device)
+    if h_final is None and h_final_index is not None:
+        raise ValueError("h_final_index needs h_final")
+    slots0, slots1 = (0 if h0 is None else h0.shape[0]), (None if h_final is None else h_final.shape[0])
+    n, cu, d, workspace = _decay_setup(lib, q, v, index, cu_seqlens, max_len, slots0, slots1, segments, workspace, 0)
     if h_final is None and want_final:
-        if h_final_index is not None:
-            raise ValueError("h_final_index needs h_final")
-        h_final = torch.empty(n, H, dk, dv, dtype=f32, device=dev)
-    slots0, slots1 = (0 if x is None else x.shape[0] for x in (h0, h_final))
-    d = _decay_desc(n, H, T, max_len, dk, dv, dt, slots0, slots1, segments, workspace)
-    r = lib.gla_decay_fwd(ctypes.byref(d), _view(q, "q", dt, (B, H, T, dk), dev), _view(k, "k", dt, (B, H, T, dk), dev),
-                          _view(v, "v", dt, (B, H, T, dv), dev), _dense_ptr(log_decay, "log_decay", f32, (H,), dev), cu,
-                          _dense_ptr(h0, "h0", f32, (slots0, H, dk, dv), dev),
-                          _dense_ptr(h0_index, "h0_index", i32, (n,), dev), _view(o, "o", dt, (B, H, T, dv), dev),
-                          _dense_ptr(h_final, "h_final", f32, (slots1, H, dk, dv), dev),
-                          _dense_ptr(h_final_index, "h_final_index", i32, (n,), dev), _stream_handle(stream))
+        h_final, slots1 = torch.empty(n, H, dk, dv, dtype=f32, device=q.device), n
+    keep, p = _views(dt, index, (q, "q", q.shape), (k, "k", q.shape), (v, "v", (B, H, T, dv)), (o, "o", (B, H, T, dv)))
+    r = lib.gla_decay_fwd(ctypes.byref(d), p, p + 32, p + 64, _dense(log_decay, "log_decay", f32, (H,), index), cu,
+                          _dense(h0, "h0", f32, (slots0, H, dk, dv), index),
+                          _dense(h0_index, "h0_index", i32, (n,), index), p + 96,
+                          _dense(h_final, "h_final", f32, (slots1, H, dk, dv), index),
+                          _dense(h_final_index, "h_final_index", i32, (n,), index), _raw_stream(stream, index))
     if r != GLA_OK:
         raise GLAError(r, "gla_decay_fwd")
     return o, h_final
@@ -680,19 +693,17 @@ def gla_decay_bwd(q, k, v, log_decay, do, *, cu_seqlens=None, max_len=None, h0=N
     lib = load()
     B, H, T, K = q.shape
     V = v.shape[-1]
-    dev, dt, f32 = q.device, q.dtype, torch.float32
-    n, max_len, cu, workspace = _decay_setup(q, v, cu_seqlens, max_len, segments, workspace, True)
+    index, dt, f32 = q.get_device(), q.dtype, torch.float32
+    n, cu, d, workspace = _decay_setup(lib, q, v, index, cu_seqlens, max_len, 0, 0, segments, workspace, 1)
     dq, dk, dv = (torch.empty_like(like) if t is None else t for t, like in ((dq, q), (dk, k), (dv, v)))
     if dh0 is None and want_dh0:
-        dh0 = torch.empty(n, H, K, V, dtype=f32, device=dev)
-    d = _decay_desc(n, H, T, max_len, K, V, dt, 0, 0, segments, workspace)
-    sk, sv, ss = (B, H, T, K), (B, H, T, V), (n, H, K, V)
-    r = lib.gla_decay_bwd(ctypes.byref(d), _view(q, "q", dt, sk, dev), _view(k, "k", dt, sk, dev),
-                          _view(v, "v", dt, sv, dev), _dense_ptr(log_decay, "log_decay", f32, (H,), dev), cu,
-                          _dense_ptr(h0, "h0", f32, ss, dev), _view(do, "do", dt, sv, dev),
-                          _dense_ptr(dh_final, "dh_final", f32, ss, dev), _view(dq, "dq", dt, sk, dev),
-                          _view(dk, "dk", dt, sk, dev), _view(dv, "dv", dt, sv, dev),
-                          _dense_ptr(dh0, "dh0", f32, ss, dev), _stream_handle(stream))
+        dh0 = torch.empty(n, H, K, V, dtype=f32, device=q.device)
+    sk, sv, ss = q.shape, (B, H, T, V), (n, H, K, V)
+    keep, p = _views(dt, index, (q, "q", sk), (k, "k", sk), (v, "v", sv), (do, "do", sv), (dq, "dq", sk), (dk, "dk", sk),
+                     (dv, "dv", sv))
+    r = lib.gla_decay_bwd(ctypes.byref(d), p, p + 32, p + 64, _dense(log_decay, "log_decay", f32, (H,), index), cu,
+                          _dense(h0, "h0", f32, ss, index), p + 96, _dense(dh_final, "dh_final", f32, ss, index),
+                          p + 128, p + 160, p + 192, _dense(dh0, "dh0", f32, ss, index), _raw_stream(stream, index))
     if r != GLA_OK:
         raise GLAError(r, "gla_decay_bwd")
     return dq, dk, dv, dh0
@@ -704,21 +715,17 @@ def gla_decay_step(q, k, v, log_decay, state, index=None, *, o=None, workspace=N
     updated in place at entry index[b] (int32; default b; negative: a padding row, left out) and
     o reads it.  q, k [B,H,dk], v [B,H,dv], any distances between rows and heads.  Returns o.
     workspace: only its status word is used (poll_status).  See include/gla.h."""
-    lib = load()
     B, H, dk = q.shape
     dv = v.shape[-1]
-    dev, dt = q.device, q.dtype
+    dev, dt, f32 = q.get_device(), q.dtype, torch.float32
     if o is None:
         # a padding row's output is not written
-        o = torch.zeros(B, H, dv, dtype=dt, device=dev) if index is not None else torch.empty(B, H, dv, dtype=dt,
-                                                                                             device=dev)
+        o = (torch.empty if index is None else torch.zeros)(B, H, dv, dtype=dt, device=q.device)
     d = _decay_desc(B, H, 1, 0, dk, dv, dt, 0, state.shape[0], 0, workspace)
-    r = lib.gla_decay_step(ctypes.byref(d), _view(q, "q", dt, (B, H, dk), dev), _view(k, "k", dt, (B, H, dk), dev),
-                           _view(v, "v", dt, (B, H, dv), dev),
-                           _dense_ptr(log_decay, "log_decay", torch.float32, (H,), dev),
-                           _dense_ptr(state, "state", torch.float32, (state.shape[0], H, dk, dv), dev),
-                           _dense_ptr(index, "index", torch.int32, (B,), dev), _view(o, "o", dt, (B, H, dv), dev),
-                           _stream_handle(stream))
+    keep, p = _views(dt, dev, (q, "q", q.shape), (k, "k", q.shape), (v, "v", (B, H, dv)), (o, "o", (B, H, dv)))
+    r = load().gla_decay_step(ctypes.byref(d), p, p + 32, p + 64, _dense(log_decay, "log_decay", f32, (H,), dev),
+                              _dense(state, "state", f32, (state.shape[0], H, dk, dv), dev),
+                              _dense(index, "index", torch.int32, (B,), dev), p + 96, _raw_stream(stream, dev))
     if r != GLA_OK:
         raise GLAError(r, "gla_decay_step")
     return o
@@ -732,9 +739,9 @@ def layernorm_workspace_size(rows, d) -> int:
     return int(n)
 
 
-def _row_view(t, name, like):
-    """(pointer, distance of rows) of [..., d] whose leading dimensions are evenly spaced rows."""
-    _like(t, name, like.dtype, like.shape, like.device)
+def _row_view(t, name, like, index):
+    """(address, distance of rows) of [..., d] whose leading dimensions are evenly spaced rows."""
+    _check(t, name, like.dtype, like.shape, index)
     if t.is_contiguous():
         return t.data_ptr(), t.shape[-1]
     if t.dim() != 2 or t.stride(1) != 1:
@@ -747,20 +754,19 @@ def gla_layernorm_fwd(x, w=None, b=None, *, eps=1e-5, y=None, want_stats=True, s
     """y = (x - mean) rstd w + b over the last dimension.  x [...,d] (contiguous, or rows of a
     wider matrix); w, b [d] fp32 or None.  Returns (y, mean, rstd), the statistics [...] in fp32
     (None without want_stats).  y may be x.  See include/gla.h."""
-    if x.dtype not in DTYPE:
+    code, shape, index, f32 = DTYPE.get(x.dtype), x.shape, x.get_device(), torch.float32
+    if code is None:
         raise ValueError(f"unsupported dtype {x.dtype}")
-    dev, n = x.device, x.shape[-1]
+    n = shape[-1]
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    mean = rstd = None
+        y = torch.empty(shape, dtype=x.dtype, device=x.device)
+    mean = rstd = pm = pr = None
     if want_stats:
-        mean, rstd = torch.empty((2,) + x.shape[:-1], dtype=torch.float32, device=dev)
-    (px, ldx), (py, ldy) = _row_view(x, "x", x), _row_view(y, "y", x)
-    r = load().gla_layernorm_fwd(DTYPE[x.dtype], x.numel() // max(1, n), n, px, ldx,
-                                 _dense_ptr(w, "w", torch.float32, (n,), dev),
-                                 _dense_ptr(b, "b", torch.float32, (n,), dev), float(eps), py, ldy,
-                                 mean.data_ptr() if want_stats else None, rstd.data_ptr() if want_stats else None,
-                                 _stream_handle(stream))
+        mean, rstd = torch.empty((2,) + shape[:-1], dtype=f32, device=x.device).unbind(0)
+        pm, pr = mean.data_ptr(), rstd.data_ptr()
+    (px, ldx), (py, ldy) = _row_view(x, "x", x, index), _row_view(y, "y", x, index)
+    r = load().gla_layernorm_fwd(code, x.numel() // max(1, n), n, px, ldx, _dense(w, "w", f32, (n,), index),
+                                 _dense(b, "b", f32, (n,), index), eps, py, ldy, pm, pr, _raw_stream(stream, index))
     if r != GLA_OK:
         raise GLAError(r, "gla_layernorm_fwd")
     return y, mean, rstd
@@ -770,27 +776,25 @@ def gla_layernorm_fwd(x, w=None, b=None, *, eps=1e-5, y=None, want_stats=True, s
 def gla_layernorm_bwd(x, dy, mean, rstd, w=None, *, dx=None, want_dwb=True, workspace=None, stream=None):
     """Backward of gla_layernorm_fwd: (dx, dw or None, db or None), dw and db [d] fp32 summed
     over all rows in a fixed order.  mean, rstd from the forward.  dx may be dy."""
-    if x.dtype not in DTYPE:
+    lib = load()
+    code, shape, index, f32 = DTYPE.get(x.dtype), x.shape, x.get_device(), torch.float32
+    if code is None:
         raise ValueError(f"unsupported dtype {x.dtype}")
-    dev, n = x.device, x.shape[-1]
+    n = shape[-1]
     rows = x.numel() // max(1, n)
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    dw = db = None
+        dx = torch.empty(shape, dtype=x.dtype, device=x.device)
+    dw = db = pw = pb = None
     if want_dwb:
-        dw, db = torch.empty(2, n, dtype=torch.float32, device=dev)
+        dw, db = torch.empty((2, n), dtype=f32, device=x.device).unbind(0)
+        pw, pb = dw.data_ptr(), db.data_ptr()
         if workspace is None:
-            workspace = alloc_workspace(layernorm_workspace_size(rows, n), dev)
-    (px, ldx), (pg, ldg), (po, ldo) = _row_view(x, "x", x), _row_view(dy, "dy", x), _row_view(dx, "dx", x)
-    f32 = torch.float32
-    r = load().gla_layernorm_bwd(DTYPE[x.dtype], rows, n, px, ldx, pg, ldg,
-                                 _dense_ptr(mean, "mean", f32, x.shape[:-1], dev),
-                                 _dense_ptr(rstd, "rstd", f32, x.shape[:-1], dev),
-                                 _dense_ptr(w, "w", f32, (n,), dev), po, ldo, dw.data_ptr() if want_dwb else None,
-                                 db.data_ptr() if want_dwb else None,
-                                 workspace.data_ptr() if workspace is not None else None,
-                                 workspace.numel() * workspace.element_size() if workspace is not None else 0,
-                                 _stream_handle(stream))
+            workspace = torch.empty(lib.gla_layernorm_workspace_size(rows, n), dtype=torch.uint8, device=x.device)
+    (px, ldx), (pg, ldg), (po, ldo) = (_row_view(t, m, x, index) for t, m in ((x, "x"), (dy, "dy"), (dx, "dx")))
+    ws, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    r = lib.gla_layernorm_bwd(code, rows, n, px, ldx, pg, ldg, _dense(mean, "mean", f32, shape[:-1], index),
+                              _dense(rstd, "rstd", f32, shape[:-1], index), _dense(w, "w", f32, (n,), index), po, ldo,
+                              pw, pb, ws, size, _raw_stream(stream, index))
     if r != GLA_OK:
         raise GLAError(r, "gla_layernorm_bwd")
     return dx, dw, db
