@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
   if (seg >= nseg || (!OUT && seg == nseg - 1)) return;
   int i0, i1;
   dev::decay_slots(w.s0, w.s1, w.alias, w.nseq, b, OUT ? w.status : nullptr, i0, i1);
-  const double rate = dev::decay_rate(w.ld, h, w.status);
+  const double rate = dev::decay_rate(__ldg(w.ld + h), w.status);
   for (int i = tid; i <= C; i += kThreads) W[i] = (float)dev::decay_pow(rate, i);
 
   // ---- start state: thread (ty, tx) owns rows 4 ty + 64 i + e, columns 4 tx .. +3
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(256) k_decay_step(int H, int nseq, int K, int 
   float4 x[kBatch];
 #pragma unroll
   for (int j = 0; j < kBatch; ++j) x[j] = load(rg + j * RG);
-  const float lam = (float)dev::decay_pow(dev::decay_rate(ld, h, status), 1);
+  const float lam = (float)dev::decay_pow(dev::decay_rate(__ldg(ld + h), status), 1);
   if (tid < K) {
     sq[tid] = to_f(((const T *)q.p)[b * q.sb + h * q.sh + tid]);
     sk[tid] = to_f(((const T *)k.p)[b * k.sb + h * k.sh + tid]);

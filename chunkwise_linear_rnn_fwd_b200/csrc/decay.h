@@ -78,8 +78,7 @@ __device__ __forceinline__ DSeq decay_seq(const DecayWalk &w, int b) {
 }
 
 // log lambda of a head: a value above zero, or NaN, is taken as zero and reported
-__device__ __forceinline__ double decay_rate(const float *ld, int h, unsigned *status) {
-  const float x = __ldg(ld + h);
+__device__ __forceinline__ double decay_rate(float x, unsigned *status) {
   if (x <= 0.f) return (double)x;
   if (threadIdx.x == 0 && status) atomicOr(status, (unsigned)ST_GATE_RANGE);
   return 0.0;
@@ -87,9 +86,11 @@ __device__ __forceinline__ double decay_rate(const float *ld, int h, unsigned *s
 // lambda^n, formed in 64 bits (n log lambda loses what matters for long spans in 32); lambda^0 = 1
 __device__ __forceinline__ double decay_pow(double rate, long n) { return n == 0 ? 1.0 : exp(rate * (double)n); }
 
-// The pool entries that sequence b reads (i0) and writes (i1), -1: none.  Every thread
-// of the CTA calls it.  One entry is written by the first sequence that names it, and a
-// sequence whose start state another one overwrites starts from zero; both are reported.
+// The pool entries that sequence b reads (i0) and writes (i1), -1: none.  One entry is
+// written by the first sequence that names it, and a sequence whose start state another one
+// overwrites starts from zero; both are reported.  Every thread of the CTA calls it, or
+// (WARP) every lane of a warp, each warp finding the answer for itself.
+template <bool WARP = false>
 __device__ __forceinline__ void decay_slots(const DPool &s0, const DPool &s1, bool alias, int nseq, int b,
                                             unsigned *status, int &i0, int &i1) {
   i0 = s0.p ? (s0.idx ? __ldg(s0.idx + b) : b) : -1;
@@ -99,21 +100,24 @@ __device__ __forceinline__ void decay_slots(const DPool &s0, const DPool &s1, bo
   if (i1 >= s1.slots) i1 = -1, bad = true;
   if (s1.idx || (alias && s0.idx)) {
     int dup = 0, hazard = 0;
-    for (int j = threadIdx.x; j < nseq; j += blockDim.x) {
+    const int me = WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x, all = WARP ? 32 : (int)blockDim.x;
+    for (int j = me; j < nseq; j += all) {
       const int wj = s1.idx ? __ldg(s1.idx + j) : j;
       dup |= j < b && wj == i1;
       hazard |= alias && j != b && wj == i0 && (i1 != i0 || j < b);
     }
     // a negative entry equals another negative one: not a use
-    dup = __syncthreads_or(dup && i1 >= 0);
-    hazard = __syncthreads_or(hazard && i0 >= 0);
+    dup = dup && i1 >= 0;
+    hazard = hazard && i0 >= 0;
+    dup = WARP ? __any_sync(0xffffffffu, dup) : __syncthreads_or(dup);
+    hazard = WARP ? __any_sync(0xffffffffu, hazard) : __syncthreads_or(hazard);
     if (dup) i1 = -1;
     if (hazard) i0 = -1;
     bad |= dup || hazard;
   }
   if (i0 < 0) i0 = -1;
   if (i1 < 0) i1 = -1;
-  if (bad && threadIdx.x == 0 && status) atomicOr(status, (unsigned)ST_INDEX);
+  if (bad && (WARP ? (threadIdx.x & 31) == 0 : threadIdx.x == 0) && status) atomicOr(status, (unsigned)ST_INDEX);
 }
 
 }  // namespace dev

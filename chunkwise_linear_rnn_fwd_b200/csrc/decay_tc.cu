@@ -135,6 +135,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long bh = blockIdx.x / tiles;
   const int b = (int)(bh / w.H), h = (int)(bh % w.H), v0 = vt * kBV;
   const int kz = OUT ? 0 : blockIdx.z;  // without outputs, 128 channels a CTA: the first block of these
+  // what the set-up reads from memory is asked for at once
+  const float ld = __ldg(w.ld + h);
+  const dev::DSeq sq = dev::decay_seq(w, b);
   if (tid == 0) {
     dev::prefetch_tmap(&tmY);
     dev::prefetch_tmap(&tmZ);
@@ -152,7 +155,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     dev::mbar_init(done, 1);
     dev::fence_mbar_init();
   }
-  const dev::DSeq sq = dev::decay_seq(w, b);
   const int n = (sq.len + kC - 1) / kC, nseg = max(1, (n + w.L - 1) / w.L);
   if (seg >= nseg || (!OUT && seg == nseg - 1)) return;  // the whole CTA
   const int c_begin = seg * w.L, nloc = max(0, min(n, c_begin + w.L) - c_begin);
@@ -189,10 +191,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     load_z(0);
   }
   if (warp == kIssueWarp) dev::tmem_alloc(tslot, kTmemCols);
-  const double rate = dev::decay_rate(w.ld, h, w.status);
+  const double rate = dev::decay_rate(ld, w.status);
   if (tid >= 128 && tid <= 128 + kC) W[tid - 128] = (float)dev::decay_pow(rate, tid - 128);
-  int i0, i1;
-  dev::decay_slots(w.s0, w.s1, w.alias, w.nseq, b, OUT ? w.status : nullptr, i0, i1);
   dev::tc_fence_before();
   __syncthreads();
   dev::tc_fence_after();
@@ -364,13 +364,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool leader = dev::elect_one();
     auto wait = [&](uint64_t *bar, uint32_t par) { return __all_sync(0xffffffffu, dev::mbar_wait(bar, par, w.status)) != 0; };
     bool ok = true;
+    // The first tiles of chunk i are looked at before the wait for P of the chunk before, so
+    // that X Y^T follows P Z without a pause.
+    auto tiles_of = [&](int i) {
+      ok = ok && wait(&xfull[slot(i, 0)], phase(i, 0)) && wait(&yfull[slot(i, 0)], phase(i, 0));
+    };
     // X Y^T of chunk i
     auto scores = [&](int i) {
       if (live_of(i) < kC) ok = ok && wait(zready, (uint32_t)(i & 1));  // Y's rows behind the sequence are cleared
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
         const int s = slot(i, kb);
-        ok = ok && wait(&xfull[s], phase(i, kb)) && wait(&yfull[s], phase(i, kb));
+        if (KB == 2) ok = ok && wait(&xfull[s], phase(i, kb)) && wait(&yfull[s], phase(i, kb));
         if (!ok) return;
         dev::tc_fence_after();
         const int ks = ksteps_of(kb);
@@ -392,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
         const int s = slot(i, kb);
-        ok = ok && wait(&xfull[s], phase(i, kb));
+        if (KB == 2) ok = ok && wait(&xfull[s], phase(i, kb));
         if (!ok) return;
         dev::tc_fence_after();
         const int ks = ksteps_of(kb);
@@ -407,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     };
+    if (OUT && KB == 1 && nloc > 0) tiles_of(0);
     for (int i = 0; i < nloc && ok; ++i) {
       const uint32_t par = (uint32_t)(i & 1);
       const int ts = (live_of(i) + 15) / 16;  // 16-token steps that hold a live token
@@ -415,13 +421,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // next Y, which has no second buffer, arrives.
       if (OUT && KB == 2) inter(i);
       if (OUT) scores(i);
-      ok = ok && wait(&zfull[i % NZ], (uint32_t)((i / NZ) & 1)) && wait(zready, par);
+      ok = ok && wait(zready, par);  // (the warps that arrive there have waited for Z)
       if (ok && i > 0) ok = wait(dsempty, par ^ 1u);
       if (!ok) break;
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
         const int s = slot(i, kb);
-        ok = ok && wait(&yfull[s], phase(i, kb));
+        if (!OUT) ok = ok && wait(&yfull[s], phase(i, kb));
         if (!ok) break;
         dev::tc_fence_after();
         const uint64_t y = dYm + s * kTileD;
@@ -442,7 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (OUT && KB == 1) inter(i);
       if (!ok) break;
       if (OUT) {
-        ok = wait(pfull, par);
+        if (KB == 1 && i + 1 < nloc) tiles_of(i + 1);
+        ok = ok && wait(pfull, par);
         if (!ok) break;
         dev::tc_fence_after();
       }
@@ -584,6 +591,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool kok = kr < w.K;
     const int nv = min(kBV, w.V - v0);  // a multiple of 8
     const bool pass = w.P > 1 && nseg > 1;
+    int i0, i1;
+    dev::decay_slots<true>(w.s0, w.s1, w.alias, w.nseq, b, OUT ? w.status : nullptr, i0, i1);
     float S[kBV];
 #pragma unroll
     for (int e = 0; e < kBV; ++e) S[e] = 0.f;

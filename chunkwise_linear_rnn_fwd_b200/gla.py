@@ -7,6 +7,7 @@ call fails, an exception is raised.  PyTorch is used only to own device memory
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import os
@@ -585,15 +586,15 @@ def _dense(t, name, dtype, shape, index):
 def _views(dtype, index, *tensors):
     """gla_view of each (tensor [B,H,T,d] or, one token, [B,H,d], its name, its shape): an array of
     them, and the address of the first (they lie 32 bytes apart)."""
-    v = []
+    a = array.array("q")
     for t, name, shape in tensors:
-        _check(t, name, dtype, shape, index)
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+            _check(t, name, dtype, shape, index)
         s = t.stride()
         if s[-1] != 1 and shape[-1] != 1:
             raise ValueError(f"{name}: the channels of a token must be contiguous")
-        v += (t.data_ptr(), s[0], s[1], s[2] if len(s) == 4 else 0)
-    a = (ctypes.c_longlong * len(v))(*v)
-    return a, ctypes.addressof(a)
+        a.extend((t.data_ptr(), s[0], s[1], s[2] if len(s) == 4 else 0))
+    return a, a.buffer_info()[0]
 
 
 def _decay_desc(B, H, T, max_len, dk, dv, dtype, slots0=0, slots1=0, segments=0, workspace=None) -> gla_decay_desc:
@@ -762,7 +763,8 @@ def gla_layernorm_fwd(x, w=None, b=None, *, eps=1e-5, y=None, want_stats=True, s
         y = torch.empty(shape, dtype=x.dtype, device=x.device)
     mean = rstd = pm = pr = None
     if want_stats:
-        mean, rstd = torch.empty((2,) + shape[:-1], dtype=f32, device=x.device).unbind(0)
+        mean = torch.empty(shape[:-1], dtype=f32, device=x.device)
+        rstd = torch.empty(shape[:-1], dtype=f32, device=x.device)
         pm, pr = mean.data_ptr(), rstd.data_ptr()
     (px, ldx), (py, ldy) = _row_view(x, "x", x, index), _row_view(y, "y", x, index)
     r = load().gla_layernorm_fwd(code, x.numel() // max(1, n), n, px, ldx, _dense(w, "w", f32, (n,), index),
@@ -786,7 +788,7 @@ def gla_layernorm_bwd(x, dy, mean, rstd, w=None, *, dx=None, want_dwb=True, work
         dx = torch.empty(shape, dtype=x.dtype, device=x.device)
     dw = db = pw = pb = None
     if want_dwb:
-        dw, db = torch.empty((2, n), dtype=f32, device=x.device).unbind(0)
+        dw, db = torch.empty(n, dtype=f32, device=x.device), torch.empty(n, dtype=f32, device=x.device)
         pw, pb = dw.data_ptr(), db.data_ptr()
         if workspace is None:
             workspace = torch.empty(lib.gla_layernorm_workspace_size(rows, n), dtype=torch.uint8, device=x.device)
