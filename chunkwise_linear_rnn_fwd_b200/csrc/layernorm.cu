@@ -5,102 +5,166 @@
 //     dx = rstd (g - mean(g) - x^ mean(g x^)) ,  dw = sum_rows dy x^ ,  db = sum_rows dy .
 //
 // Bound by HBM: the forward reads x and writes y, the backward reads x and dy and writes
-// dx.  A row stays in the registers of a group of G threads (a warp, or a whole CTA for
-// wide rows), so it is read once: 16-byte loads where the data, the distance of rows and d
-// allow, single values otherwise.  The backward keeps the sums over rows for its columns
-// in registers while it strides over the rows and leaves one partial sum per CTA; a second
-// kernel adds those in a fixed order.
+// dx.  A row belongs to a group of G threads that hold it in registers, so it is read once:
+// 16-byte loads where the data, the distance of rows and d allow, pairs of single values
+// otherwise.  A CTA of 512 threads stays for many rows, its groups take them in turn, R at a time.
+// Forward: up to 64 values a thread, a warp a row up to 2048 bf16 values, so that the sums
+// over a row's threads are a small part.  Backward: 8 values a thread, because each costs
+// two more registers for its columns' sums over all rows, and what hides the latency here is the number of
+// warps: with 32 values a thread, a quarter of the warps, 16384 rows of 1024 took 57 us
+// instead of 37, and rings of prefetched rows in shared memory did not make up for it.  The sums
+// over the threads of a row are formed for R rows together.  The backward leaves one partial
+// sum of dw and db per CTA, which a second kernel adds in a fixed order.
 #include <cuda_bf16.h>
 
 #include "internal.h"
+#include "tc_common.cuh"
 
 namespace gla {
 namespace {
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
+// The arithmetic runs on pairs of fp32 values (f32x2: one instruction for two), which halves
+// the instructions: at two bytes a value these kernels were bound by them.
+using dev::add2;
+using dev::bf16pair;
+using dev::f2;
+using dev::fma2;
+using dev::hsum;
+using dev::mul2;
+using dev::pk;
+using dev::upk;
 
-// VEC consecutive values as fp32 (VEC elements of T are 16 bytes, or one element)
-template <int VEC>
-__device__ __forceinline__ void ldv(const float *p, float *v) {
-  if constexpr (VEC == 1) {
-    v[0] = __ldg(p);
-  } else {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    if constexpr (VEC == 8) {
-      const float4 c = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-      v[4] = c.x, v[5] = c.y, v[6] = c.z, v[7] = c.w;
-    }
-  }
-}
-// x may be y and dy may be dx (in place): these are not read through the read-only path
+// VEC consecutive values of a tensor, 16 bytes or two values, as P pairs.  x may be y and dy
+// may be dx (in place), so the loads are ordinary ones.
 template <typename T, int VEC>
 struct Pack;
 template <>
 struct Pack<float, 4> {
-  float4 a;
-  __device__ __forceinline__ void load(const float *p) { a = *reinterpret_cast<const float4 *>(p); }
-  __device__ __forceinline__ void get(float *v) const { v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w; }
-  __device__ __forceinline__ void put(const float *v) { a = make_float4(v[0], v[1], v[2], v[3]); }
-  __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<float4 *>(p) = a; }
+  static constexpr int P = 2;
+  ulonglong2 a;
+  __device__ __forceinline__ void load(const float *p) { a = *reinterpret_cast<const ulonglong2 *>(p); }
+  __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<ulonglong2 *>(p) = a; }
+  __device__ __forceinline__ f2 get(int i) const { return i ? a.y : a.x; }
+  __device__ __forceinline__ void put(int i, f2 v) { (i ? a.y : a.x) = v; }
 };
 template <>
 struct Pack<__nv_bfloat16, 8> {
-  uint4 a;
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = *reinterpret_cast<const uint4 *>(p); }
-  __device__ __forceinline__ void get(float *v) const {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+  static constexpr int P = 4;
+  uint32_t a[4];
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+    a[0] = u.x, a[1] = u.y, a[2] = u.z, a[3] = u.w;
   }
-  __device__ __forceinline__ void put(const float *v) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-    a = make_uint4(w[0], w[1], w[2], w[3]);
+  __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(a[0], a[1], a[2], a[3]);
   }
-  __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *reinterpret_cast<uint4 *>(p) = a; }
+  __device__ __forceinline__ f2 get(int i) const { return bf16pair(a[i]); }
+  __device__ __forceinline__ void put(int i, f2 v) {
+    float lo, hi;
+    upk(v, lo, hi);
+    a[i] = dev::pack_bf16(lo, hi);
+  }
+};
+// two values loaded one by one; the second is absent (zero, not stored) behind a row's end
+template <>
+struct Pack<float, 2> {
+  static constexpr int P = 1;
+  f2 a;
+  __device__ __forceinline__ void load(const float *p, bool both) { a = pk(p[0], both ? p[1] : 0.f); }
+  __device__ __forceinline__ void store(float *p, bool both) const {
+    float lo, hi;
+    upk(a, lo, hi);
+    p[0] = lo;
+    if (both) p[1] = hi;
+  }
+  __device__ __forceinline__ f2 get(int) const { return a; }
+  __device__ __forceinline__ void put(int, f2 v) { a = v; }
 };
 template <>
-struct Pack<float, 1> {
-  float a;
-  __device__ __forceinline__ void load(const float *p) { a = *p; }
-  __device__ __forceinline__ void get(float *v) const { v[0] = a; }
-  __device__ __forceinline__ void put(const float *v) { a = v[0]; }
-  __device__ __forceinline__ void store(float *p) const { *p = a; }
+struct Pack<__nv_bfloat16, 2> {
+  static constexpr int P = 1;
+  uint32_t a;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p, bool both) {
+    const unsigned short *u = reinterpret_cast<const unsigned short *>(p);
+    a = u[0] | (both ? (uint32_t)u[1] << 16 : 0u);
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16 *p, bool both) const {
+    unsigned short *u = reinterpret_cast<unsigned short *>(p);
+    u[0] = (unsigned short)(a & 0xffffu);
+    if (both) u[1] = (unsigned short)(a >> 16);
+  }
+  __device__ __forceinline__ f2 get(int) const { return bf16pair(a); }
+  __device__ __forceinline__ void put(int, f2 v) {
+    float lo, hi;
+    upk(v, lo, hi);
+    a = dev::pack_bf16(lo, hi);
+  }
 };
-template <>
-struct Pack<__nv_bfloat16, 1> {
-  __nv_bfloat16 a;
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = *p; }
-  __device__ __forceinline__ void get(float *v) const { v[0] = __bfloat162float(a); }
-  __device__ __forceinline__ void put(const float *v) { a = __float2bfloat16_rn(v[0]); }
-  __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *p = a; }
-};
+template <typename T, int VEC>
+__device__ __forceinline__ void load_pack(Pack<T, VEC> &p, const T *x, int c, int d) {
+  if constexpr (VEC == 2) p.load(x + c, c + 1 < d);
+  else p.load(x + c);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_pack(const Pack<T, VEC> &p, T *x, int c, int d) {
+  if constexpr (VEC == 2) p.store(x + c, c + 1 < d);
+  else p.store(x + c);
+}
+// P pairs of weights from column c on (`none` without weights, zero behind the end)
+template <int VEC, int P>
+__device__ __forceinline__ void weights_of(const float *p, float none, int c, int d, f2 *v) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) v[i] = pk(none, none);
+  if (!p || c >= d) return;
+  if constexpr (VEC == 2) {
+    v[0] = pk(__ldg(p + c), c + 1 < d ? __ldg(p + c + 1) : 0.f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; i += 2) {
+      const ulonglong2 u = __ldg(reinterpret_cast<const ulonglong2 *>(p + c + 2 * i));
+      v[i] = u.x, v[i + 1] = u.y;
+    }
+  }
+}
 
-// Sum over a group of G threads (G <= 32: within a warp; else the whole CTA of G threads,
-// through `red`; every use gets its own slot of red, so one barrier a sum is enough)
-template <int G>
-__device__ __forceinline__ float group_sum(float x, float *red) {
-  x = warp_sum(x);
-  if constexpr (G > 32) {
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = 0.f;
+constexpr int kLnThreads = 512;
+constexpr int kLnCtas = 296;  // two on each of 148 SMs; also the most partial sums of a backward
+
+// Sums of V values (V a power of two up to 8) over a group of G threads, each thread getting
+// all of them.  Within a warp the values halve while the lanes they are summed over double:
+// V - 1 exchanges and one more per halving that is left, not five a value.  Lane l then holds
+// value l mod V.  Then through red[group][G / 32][V]; a group's threads alone meet at its barrier.
+template <int G, int V>
+__device__ __forceinline__ void group_sums(float (&x)[V], float *red) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < G / 32; ++i) x += red[i];
+  for (int half = V / 2; half >= 1; half /= 2) {
+    const bool up = (lane & half) != 0;
+#pragma unroll
+    for (int j = 0; j < half; ++j) {
+      const float send = up ? x[j] : x[j + half], keep = up ? x[j + half] : x[j];
+      x[j] = keep + __shfl_xor_sync(0xffffffffu, send, half);
+    }
   }
-  return x;
+  float s = x[0];
+#pragma unroll
+  for (int o = V; o < 32; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if constexpr (G > 32) {
+    constexpr int W = G / 32;
+    const int group = threadIdx.x / G, warp = (threadIdx.x % G) >> 5;
+    float *mine = red + group * W * V;
+    if (lane < V) mine[warp * V + lane] = s;
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(G) : "memory");
+    // lane l adds value l mod V of the warps l / V, l / V + 32 / V, .. and the lanes the rest
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < W * V; i += 32)
+      if (i + lane < W * V) s += mine[i + lane];
+#pragma unroll
+    for (int o = V; o < 32 && o < W * V; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) x[j] = __shfl_sync(0xffffffffu, s, j);
 }
 
 struct LnArgs {
@@ -116,210 +180,203 @@ struct LnArgs {
   float *part;                 // [CTAs][2][d]
 };
 
-constexpr int kLnThreads = 256;
+// CTAs of 512 threads that an SM holds: two while the values of a thread leave room in 64 registers
+template <int VEC, int N, int R, bool BWD>
+constexpr int ctas_per_sm() {
+  return BWD ? (N * VEC <= 8 ? 2 : 1) : (N * VEC * R <= 16 ? 2 : 1);
+}
 
-// G threads hold N packs of VEC values of a row each.
-template <typename T, int VEC, int N, int G>
-__global__ void __launch_bounds__(G < kLnThreads ? kLnThreads : G) k_ln_fwd(LnArgs a) {
-  __shared__ float red[2][32];
-  constexpr int kGroups = G < kLnThreads ? kLnThreads / G : 1;
-  const int t = threadIdx.x % G;
-  const long row = (long)blockIdx.x * kGroups + threadIdx.x / G;
-  if (row >= a.rows) return;  // a whole warp, or the whole CTA
-  const T *x = (const T *)a.x + row * a.ldx;
-  T *y = (T *)a.out + row * a.ldo;
-  Pack<T, VEC> p[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int c = VEC * (t + G * i);
-    if (c < a.d) p[i].load(x + c);
-  }
+template <typename T, int VEC, int N, int G, int R>
+__global__ void __launch_bounds__(kLnThreads, ctas_per_sm<VEC, N, R, false>()) k_ln_fwd(LnArgs a) {
+  constexpr int kGroups = kLnThreads / G, P = Pack<T, VEC>::P;
+  // two places in turn: a thread past the barrier of one sum cannot reach the writes of the
+  // sum after the next before every thread of its group has passed the next one's barrier
+  __shared__ float red[2][kGroups * R * (G / 32)];
+  const int t = threadIdx.x % G, group = threadIdx.x / G;
   const float inv = 1.f / (float)a.d;
-  float s = 0.f;
+  const long step = (long)gridDim.x * kGroups * R;
+  for (long row0 = ((long)group * gridDim.x + blockIdx.x) * R; row0 < a.rows; row0 += step) {
+    Pack<T, VEC> p[R][N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float v[VEC];
-    p[i].get(v);
-    if (VEC * (t + G * i) < a.d)
+    for (int r = 0; r < R; ++r) {
+      const T *x = (const T *)a.x + (row0 + r) * a.ldx;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) s += v[e];
-  }
-  const float mean = group_sum<G>(s, red[0]) * inv;
-  float q = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float v[VEC];
-    p[i].get(v);
-    if (VEC * (t + G * i) < a.d)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) q = fmaf(v[e] - mean, v[e] - mean, q);
-  }
-  const float rstd = rsqrtf(group_sum<G>(q, red[1]) * inv + a.eps);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int c = VEC * (t + G * i);
-    if (c < a.d) {
-      float v[VEC], w[VEC], b[VEC];
-      p[i].get(v);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) w[e] = 1.f, b[e] = 0.f;
-      if (a.w) ldv<VEC>(a.w + c, w);
-      if (a.b) ldv<VEC>(a.b + c, b);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) v[e] = fmaf((v[e] - mean) * rstd, w[e], b[e]);
-      p[i].put(v);
-      p[i].store(y + c);
+      for (int i = 0; i < N; ++i) {
+        const int c = VEC * (t + G * i);
+        if (c < a.d && row0 + r < a.rows) load_pack(p[r][i], x, c, a.d);
+      }
     }
-  }
-  if (t == 0) {
-    if (a.mean) a.mean[row] = mean;
-    if (a.rstd) a.rstd[row] = rstd;
+    float mean[R], rstd[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      f2 s = pk(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (VEC * (t + G * i) < a.d)
+#pragma unroll
+          for (int e = 0; e < P; ++e) s = add2(s, p[r][i].get(e));
+      mean[r] = hsum(s);
+    }
+    group_sums<G, R>(mean, red[0]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mean[r] *= inv;
+      const f2 nm = pk(-mean[r], -mean[r]);
+      f2 s = pk(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int c = VEC * (t + G * i);
+        if (c < a.d)
+#pragma unroll
+          for (int e = 0; e < P; ++e) {
+            const f2 v = add2(p[r][i].get(e), VEC == 2 && c + 1 >= a.d ? pk(-mean[r], 0.f) : nm);
+            s = fma2(v, v, s);
+          }
+      }
+      rstd[r] = hsum(s);
+    }
+    group_sums<G, R>(rstd, red[1]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      rstd[r] = rsqrtf(rstd[r] * inv + a.eps);
+      if (t == 0 && row0 + r < a.rows) {
+        if (a.mean) a.mean[row0 + r] = mean[r];
+        if (a.rstd) a.rstd[row0 + r] = rstd[r];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = VEC * (t + G * i);
+      f2 w[P], b[P];
+      weights_of<VEC, P>(a.w, 1.f, c, a.d, w);
+      weights_of<VEC, P>(a.b, 0.f, c, a.d, b);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const f2 nm = pk(-mean[r], -mean[r]), rs = pk(rstd[r], rstd[r]);
+#pragma unroll
+        for (int e = 0; e < P; ++e) p[r][i].put(e, fma2(mul2(add2(p[r][i].get(e), nm), rs), w[e], b[e]));
+        if (c < a.d && row0 + r < a.rows) store_pack(p[r][i], (T *)a.out + (row0 + r) * a.ldo, c, a.d);
+      }
+    }
   }
 }
 
-// A group of G threads (a warp, or the whole CTA for wide rows) takes R rows at a time;
-// thread t of it owns the columns VEC (t + G i) .. in every row and carries their sums of
-// dy x^ and dy.  The next rows' loads are issued before these are worked on.
+// The groups of a backward CTA add up their sums in shared memory; the two groups of rows too
+// wide for that, in the partial sum's own place.
+template <int VEC, int N, int G>
+__host__ __device__ constexpr bool sums_in_smem() {
+  return G < kLnThreads && 2 * VEC * N * G * sizeof(float) <= 40 * 1024;
+}
+
+// Thread t of a group carries its columns' sums of dy x^ and dy over all of its rows.
 template <typename T, int VEC, int N, int G, int R>
-__global__ void __launch_bounds__(G < kLnThreads ? kLnThreads : G, G <= kLnThreads ? 2 : 1) k_ln_bwd(LnArgs a) {
-  constexpr int kGroups = G < kLnThreads ? kLnThreads / G : 1;
-  __shared__ float2 red[2][R][32];
-  extern __shared__ float sums[];  // [groups][2][d], with more than one group
-  const int t = threadIdx.x % G, warp = threadIdx.x >> 5, group = threadIdx.x / G;
+__global__ void __launch_bounds__(kLnThreads, ctas_per_sm<VEC, N, R, true>()) k_ln_bwd(LnArgs a) {
+  constexpr int kGroups = kLnThreads / G, P = Pack<T, VEC>::P;
+  __shared__ float red[2][kGroups * 2 * R * (G / 32)];  // in turn, as in the forward: one barrier a round
+  extern __shared__ float shared_sums[];                // [2][d] (sums_in_smem)
+  const int t = threadIdx.x % G, group = threadIdx.x / G;
   const float inv = 1.f / (float)a.d;
+  const f2 zero = pk(0.f, 0.f);
   const long step = (long)gridDim.x * kGroups * R;
-  float dw[N * VEC], db[N * VEC];
+  f2 dw[N * P], db[N * P];
 #pragma unroll
-  for (int i = 0; i < N * VEC; ++i) dw[i] = db[i] = 0.f;
-  // wide rows (many values a thread) keep neither the weights nor the next rows
-  constexpr bool kKeep = N * VEC <= 16;
-  struct Rows {
-    Pack<T, VEC> x[R][N], g[R][N];
+  for (int i = 0; i < N * P; ++i) dw[i] = db[i] = zero;
+  constexpr bool kKeep = N * VEC * R <= 8;  // the weights stay in registers
+  f2 wk[kKeep ? N * P : P];
+  if constexpr (kKeep)
+#pragma unroll
+    for (int i = 0; i < N; ++i) weights_of<VEC, P>(a.w, 1.f, VEC * (t + G * i), a.d, wk + i * P);
+  int par = 0;
+  for (long row0 = ((long)group * gridDim.x + blockIdx.x) * R; row0 < a.rows; row0 += step, par ^= 1) {
+    Pack<T, VEC> px[R][N], pg[R][N];
     float mean[R], rstd[R];
-  };
-  auto load = [&](Rows &p, long row0) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const long row = row0 + r;
-      p.mean[r] = p.rstd[r] = 0.f;
+      mean[r] = rstd[r] = 0.f;
       if (row < a.rows) {
         const T *x = (const T *)a.x + row * a.ldx, *dy = (const T *)a.dy + row * a.lddy;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const int c = VEC * (t + G * i);
-          if (c < a.d) p.x[r][i].load(x + c), p.g[r][i].load(dy + c);
+          if (c < a.d) load_pack(px[r][i], x, c, a.d), load_pack(pg[r][i], dy, c, a.d);
         }
-        p.mean[r] = __ldg(a.cmean + row);
-        p.rstd[r] = __ldg(a.crstd + row);
+        mean[r] = __ldg(a.cmean + row);
+        rstd[r] = __ldg(a.crstd + row);
       }
     }
-  };
-  float kept[kKeep ? N * VEC : 1];
-  auto weights = [&](int i, float *w) {
-    const int c = VEC * (t + G * i);
+    float s[2 * R];  // sums of g and of g x^ (an absent value's dy and weight are zero)
+    f2 s1[R], s2[R];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) w[e] = 1.f;
-    if (c < a.d && a.w) ldv<VEC>(a.w + c, w);
-  };
-  if constexpr (kKeep)
-#pragma unroll
-    for (int i = 0; i < N; ++i) weights(i, kept + i * VEC);
-  int par = 0;
-  long row0 = ((long)blockIdx.x * kGroups + group) * R;
-  Rows p;
-  load(p, row0);
-  // (G > 32: one group a CTA, so that every thread makes the same number of rounds)
-  for (; row0 < a.rows; row0 += step, par ^= 1) {
-    Rows next;
-    if constexpr (kKeep) load(next, row0 + step);
-    float s1[R], s2[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) s1[r] = s2[r] = 0.f;
+    for (int r = 0; r < R; ++r) s1[r] = s2[r] = zero;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = VEC * (t + G * i);
-      float w[VEC];
-      if constexpr (!kKeep) weights(i, w);
+      f2 *w = wk + (kKeep ? i * P : 0);
+      if constexpr (!kKeep) weights_of<VEC, P>(a.w, 1.f, c, a.d, w);
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
+      for (int r = 0; r < R; ++r)
         if (c < a.d && row0 + r < a.rows) {
-          float xv[VEC], gv[VEC];
-          p.x[r][i].get(xv);
-          p.g[r][i].get(gv);
+          const f2 nm = pk(-mean[r], -mean[r]), rs = pk(rstd[r], rstd[r]);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float h = (xv[e] - p.mean[r]) * p.rstd[r], g = gv[e] * (kKeep ? kept[kKeep ? i * VEC + e : 0] : w[e]);
-            dw[i * VEC + e] = fmaf(gv[e], h, dw[i * VEC + e]);
-            db[i * VEC + e] += gv[e];
-            s1[r] += g;
-            s2[r] = fmaf(g, h, s2[r]);
+          for (int e = 0; e < P; ++e) {
+            const f2 h = mul2(add2(px[r][i].get(e), nm), rs), dy = pg[r][i].get(e), g = mul2(dy, w[e]);
+            dw[i * P + e] = fma2(dy, h, dw[i * P + e]);
+            db[i * P + e] = add2(db[i * P + e], dy);
+            s1[r] = add2(s1[r], g);
+            s2[r] = fma2(g, h, s2[r]);
           }
         }
-      }
     }
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      s1[r] = warp_sum(s1[r]);
-      s2[r] = warp_sum(s2[r]);
-    }
-    if constexpr (G > 32) {
-      // two buffers in turn: a thread past the barrier of one round cannot reach the writes
-      // of the round after the next before every thread has passed the next one's barrier
-      if ((t & 31) == 0)
-#pragma unroll
-        for (int r = 0; r < R; ++r) red[par][r][warp] = make_float2(s1[r], s2[r]);
-      __syncthreads();
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        s1[r] = s2[r] = 0.f;
-#pragma unroll
-        for (int i = 0; i < G / 32; ++i) s1[r] += red[par][r][i].x, s2[r] += red[par][r][i].y;
-      }
-    }
+    for (int r = 0; r < R; ++r) s[2 * r] = hsum(s1[r]), s[2 * r + 1] = hsum(s2[r]);
+    group_sums<G, 2 * R>(s, red[par]);
+    // dx = rstd g - rstd mean(g) - x^ rstd mean(g x^), x^ = x rstd - mean rstd
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = VEC * (t + G * i);
-      float w[VEC];
-      if constexpr (!kKeep) weights(i, w);
+      f2 *w = wk + (kKeep ? i * P : 0);
+      if constexpr (!kKeep) weights_of<VEC, P>(a.w, 1.f, c, a.d, w);
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
+      for (int r = 0; r < R; ++r)
         if (c < a.d && row0 + r < a.rows) {
-          const float m1 = s1[r] * inv, m2 = s2[r] * inv;
-          float xv[VEC], gv[VEC];
-          p.x[r][i].get(xv);
-          p.g[r][i].get(gv);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float h = (xv[e] - p.mean[r]) * p.rstd[r], g = gv[e] * (kKeep ? kept[kKeep ? i * VEC + e : 0] : w[e]);
-            xv[e] = p.rstd[r] * (g - m1 - h * m2);
-          }
+          const float mx = -rstd[r] * rstd[r] * (s[2 * r + 1] * inv), m1 = -rstd[r] * (s[2 * r] * inv) - mean[r] * mx;
+          const f2 rs = pk(rstd[r], rstd[r]), c1 = pk(m1, m1), cx = pk(mx, mx);
           Pack<T, VEC> out;
-          out.put(xv);
-          out.store((T *)a.out + (row0 + r) * a.ldo + c);
+#pragma unroll
+          for (int e = 0; e < P; ++e) {
+            const f2 g = mul2(pg[r][i].get(e), w[e]);
+            out.put(e, fma2(g, rs, fma2(px[r][i].get(e), cx, c1)));
+          }
+          store_pack(out, (T *)a.out + (row0 + r) * a.ldo, c, a.d);
         }
-      }
     }
-    if constexpr (kKeep) p = next;
-    else load(p, row0 + step);
   }
   if (!a.part) return;
-  float *part = a.part + (long)blockIdx.x * 2 * a.d;
-  float *mine = kGroups > 1 ? sums + (long)group * 2 * a.d : part;
+  float *part = a.part + (long)blockIdx.x * 2 * a.d, *sums = sums_in_smem<VEC, N, G>() ? shared_sums : part;
+  // the CTA's groups in order
+#pragma unroll 1
+  for (int g = 0; g < kGroups; ++g) {
+    if (g == group) {
 #pragma unroll
-  for (int i = 0; i < N; ++i)
+      for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int c = VEC * (t + G * i) + e;
-      if (c < a.d) mine[c] = dw[i * VEC + e], mine[a.d + c] = db[i * VEC + e];
+        for (int e = 0; e < P; ++e) {
+          float u[2], v[2];
+          upk(dw[i * P + e], u[0], u[1]);
+          upk(db[i * P + e], v[0], v[1]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int c = VEC * (t + G * i) + 2 * e + k;
+            if (c < a.d) {
+              if (g > 0) u[k] += sums[c], v[k] += sums[a.d + c];
+              float *to = g == kGroups - 1 ? part : sums;
+              to[c] = u[k], to[a.d + c] = v[k];
+            }
+          }
+        }
     }
-  if constexpr (kGroups > 1) {  // the CTA's groups in order
-    __syncthreads();
-    for (int c = threadIdx.x; c < 2 * a.d; c += kLnThreads) {
-      float s = 0.f;
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) s += sums[(long)g * 2 * a.d + c];
-      part[c] = s;
-    }
+    if (kGroups > 1) __syncthreads();
   }
 }
 
@@ -348,54 +405,53 @@ __global__ void __launch_bounds__(1024) k_ln_reduce(int parts, int d, const floa
   }
 }
 
-constexpr int kBwdCtas = 296;  // partial sums of a backward at most: two CTAs on each of 148 SMs
-
-long bwd_ctas(long rows) { return rows < kBwdCtas ? rows : kBwdCtas; }
-
-template <typename T, int VEC, int N, int G>
-int fwd_launch(const LnArgs &a, cudaStream_t st) {
-  constexpr int kGroups = G < kLnThreads ? kLnThreads / G : 1;
-  const long grid = (a.rows + kGroups - 1) / kGroups;
-  GLA_LAUNCH(K_LN_FWD, st, (k_ln_fwd<T, VEC, N, G><<<(unsigned)grid, G < kLnThreads ? kLnThreads : G, 0, st>>>(a)));
+template <typename T, int VEC, int N, int G, int R, bool BWD>
+int launch(const LnArgs &a, float *dw, float *db, cudaStream_t st) {
+  // rows go to the CTAs first, then to their groups
+  const long rounds = (a.rows + R - 1) / R, most = 148 * ctas_per_sm<VEC, N, R, BWD>();
+  const unsigned grid = (unsigned)(rounds < most ? rounds : most);
+  if constexpr (BWD) {
+    const size_t smem = sums_in_smem<VEC, N, G>() && a.part ? (size_t)2 * a.d * sizeof(float) : 0;
+    GLA_LAUNCH(K_LN_BWD, st, (k_ln_bwd<T, VEC, N, G, R><<<grid, kLnThreads, smem, st>>>(a)));
+    if (a.part)
+      GLA_LAUNCH(K_LN_REDUCE, st, (k_ln_reduce<<<(2 * a.d + 31) / 32, 1024, 0, st>>>((int)grid, a.d, a.part, dw, db)));
+  } else {
+    GLA_LAUNCH(K_LN_FWD, st, (k_ln_fwd<T, VEC, N, G, R><<<grid, kLnThreads, 0, st>>>(a)));
+  }
   return GLA_OK;
 }
 
-template <typename T, int VEC, int N, int G, int R>
-int bwd_launch(const LnArgs &a, float *dw, float *db, cudaStream_t st) {
-  constexpr int kGroups = G < kLnThreads ? kLnThreads / G : 1;
-  const long rounds = (a.rows + kGroups * R - 1) / (kGroups * R), most = bwd_ctas(a.rows);
-  const long grid = rounds < most ? rounds : most;
-  const size_t smem = kGroups > 1 && a.part ? (size_t)kGroups * 2 * a.d * sizeof(float) : 0;
-  GLA_LAUNCH(K_LN_BWD, st, (k_ln_bwd<T, VEC, N, G, R><<<(unsigned)grid, G < kLnThreads ? kLnThreads : G, smem, st>>>(a)));
-  if (a.part)
-    GLA_LAUNCH(K_LN_REDUCE, st, (k_ln_reduce<<<(2 * a.d + 31) / 32, 1024, 0, st>>>((int)grid, a.d, a.part, dw, db)));
-  return GLA_OK;
+// R rows at a time once there are enough for every group on the GPU
+template <typename T, int VEC, int N, int G, int R, bool BWD>
+int rows_of(const LnArgs &a, float *dw, float *db, cudaStream_t st) {
+  if constexpr (R > 1)
+    if (a.rows <= (long)kLnCtas * (kLnThreads / G) * R / 2) return launch<T, VEC, N, G, 1, BWD>(a, dw, db, st);
+  return launch<T, VEC, N, G, R, BWD>(a, dw, db, st);
 }
 
-// Rows up to 2048 values wide (512 single ones) to a warp each, wider ones to a CTA.
-template <typename T, int VEC>
-int fwd_t(const LnArgs &a, cudaStream_t st) {
-  const int n = (a.d + VEC - 1) / VEC;  // packs of a row
-  constexpr int F = VEC == 1 ? 4 : VEC == 4 ? 2 : 1;  // packs per thread that make 8 values, or 4 single ones
-  if (n <= 32 * F) return fwd_launch<T, VEC, F, 32>(a, st);
-  if (n <= 32 * 4 * F) return fwd_launch<T, VEC, 4 * F, 32>(a, st);
-  if constexpr (VEC > 1)
-    if (n <= 32 * 8 * F) return fwd_launch<T, VEC, 8 * F, 32>(a, st);
-  if (n <= 256 * 2 * F) return fwd_launch<T, VEC, 2 * F, 256>(a, st);
-  return fwd_launch<T, VEC, 4 * F, VEC == 1 ? 1024 : 512>(a, st);
-}
-// Rows up to 512 values (128 single ones) to a warp each.  Four rows at a time keep 64 KB in
-// flight on an SM; wide rows do with fewer.
-template <typename T, int VEC>
-int bwd_t(const LnArgs &a, float *dw, float *db, cudaStream_t st) {
-  const int n = (a.d + VEC - 1) / VEC;
-  constexpr int F = VEC == 1 ? 4 : VEC == 4 ? 2 : 1;
-  if (n <= 32 * F) return bwd_launch<T, VEC, F, 32, 4>(a, dw, db, st);
-  if constexpr (VEC > 1)
-    if (n <= 64 * F) return bwd_launch<T, VEC, 2 * F, 32, 2>(a, dw, db, st);
-  if (n <= 256 * F) return bwd_launch<T, VEC, F, 256, 4>(a, dw, db, st);
-  if (n <= 512 * 2 * F) return bwd_launch<T, VEC, 2 * F, 512, 1>(a, dw, db, st);
-  return bwd_launch<T, VEC, VEC == 1 ? 8 * F : 4 * F, 512, 1>(a, dw, db, st);
+// N packs a thread: a warp a row while that suffices (more rows at a time where less does),
+// then 64 to 512 threads a row, then 512 threads with more packs.
+template <typename T, int VEC, bool BWD>
+int run(const LnArgs &a, float *dw, float *db, cudaStream_t st) {
+  if constexpr (BWD || VEC == 2) {
+    constexpr int N = 8 / VEC, W = 32 * VEC * N, R = sizeof(T) == 2 ? 2 : 1;
+    if (a.d <= W) return rows_of<T, VEC, N, 32, R, BWD>(a, dw, db, st);
+    if (a.d <= 2 * W) return rows_of<T, VEC, N, 64, R, BWD>(a, dw, db, st);
+    if (a.d <= 4 * W) return rows_of<T, VEC, N, 128, R, BWD>(a, dw, db, st);
+    if (a.d <= 8 * W) return rows_of<T, VEC, N, 256, R, BWD>(a, dw, db, st);
+    if (a.d <= 16 * W) return rows_of<T, VEC, N, 512, R, BWD>(a, dw, db, st);
+    if (a.d <= 32 * W) return rows_of<T, VEC, 2 * N, 512, 1, BWD>(a, dw, db, st);
+    return rows_of<T, VEC, 4 * N, 512, 1, BWD>(a, dw, db, st);
+  } else {
+    constexpr int N = 8, W = 32 * VEC * N;
+    if (a.d <= W / 4) return rows_of<T, VEC, 2, 32, 4, BWD>(a, dw, db, st);
+    if (a.d <= W / 2) return rows_of<T, VEC, 4, 32, 4, BWD>(a, dw, db, st);
+    if (a.d <= W) return rows_of<T, VEC, N, 32, VEC == 8 ? 2 : 1, BWD>(a, dw, db, st);
+    if (a.d <= 2 * W) return rows_of<T, VEC, N, 64, 1, BWD>(a, dw, db, st);
+    if (a.d <= 4 * W) return rows_of<T, VEC, N, 128, 1, BWD>(a, dw, db, st);
+    if (a.d <= 8 * W) return rows_of<T, VEC, N, 256, 1, BWD>(a, dw, db, st);
+    return rows_of<T, VEC, N, 512, 1, BWD>(a, dw, db, st);
+  }
 }
 
 bool al16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
@@ -426,7 +482,7 @@ extern "C" {
 
 size_t gla_layernorm_workspace_size(long long rows, int d) {
   if (check(GLA_DTYPE_FP32, rows, d) != GLA_OK) return 0;
-  return align_up((size_t)bwd_ctas(rows) * 2 * d * sizeof(float), 256);
+  return align_up((size_t)(rows < kLnCtas ? rows : kLnCtas) * 2 * d * sizeof(float), 256);
 }
 
 int gla_layernorm_fwd(int dtype, long long rows, int d, const void *x, long long ldx, const float *w, const float *b,
@@ -442,8 +498,9 @@ int gla_layernorm_fwd(int dtype, long long rows, int d, const void *x, long long
   const int vec = dtype == GLA_DTYPE_BF16 ? 8 : 4;
   const bool wide = d % vec == 0 && ldx % vec == 0 && ldy % vec == 0 && al16(x) && al16(y) && al16(w) && al16(b);
   cudaStream_t st = (cudaStream_t)stream;
-  if (dtype == GLA_DTYPE_BF16) return wide ? fwd_t<__nv_bfloat16, 8>(a, st) : fwd_t<__nv_bfloat16, 1>(a, st);
-  return wide ? fwd_t<float, 4>(a, st) : fwd_t<float, 1>(a, st);
+  if (dtype == GLA_DTYPE_BF16)
+    return wide ? run<__nv_bfloat16, 8, false>(a, nullptr, nullptr, st) : run<__nv_bfloat16, 2, false>(a, nullptr, nullptr, st);
+  return wide ? run<float, 4, false>(a, nullptr, nullptr, st) : run<float, 2, false>(a, nullptr, nullptr, st);
 }
 
 int gla_layernorm_bwd(int dtype, long long rows, int d, const void *x, long long ldx, const void *dy, long long lddy,
@@ -469,8 +526,8 @@ int gla_layernorm_bwd(int dtype, long long rows, int d, const void *x, long long
                     al16(dx) && al16(w);
   cudaStream_t st = (cudaStream_t)stream;
   if (dtype == GLA_DTYPE_BF16)
-    return wide ? bwd_t<__nv_bfloat16, 8>(a, dw, db, st) : bwd_t<__nv_bfloat16, 1>(a, dw, db, st);
-  return wide ? bwd_t<float, 4>(a, dw, db, st) : bwd_t<float, 1>(a, dw, db, st);
+    return wide ? run<__nv_bfloat16, 8, true>(a, dw, db, st) : run<__nv_bfloat16, 2, true>(a, dw, db, st);
+  return wide ? run<float, 4, true>(a, dw, db, st) : run<float, 2, true>(a, dw, db, st);
 }
 
 }  // extern "C"
