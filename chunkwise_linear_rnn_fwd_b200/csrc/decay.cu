@@ -451,6 +451,7 @@ int check_view(const gla_view *v, int dtype, DView *out) {
   return GLA_OK;
 }
 
+int check_words(const void *p) { return (uintptr_t)p & 3u ? GLA_ERR_MISALIGNED : GLA_OK; }
 int check_states(const float *p) { return ((uintptr_t)p & 15u) ? GLA_ERR_MISALIGNED : GLA_OK; }
 
 DPool pool(const float *p, const int *idx, int slots, const gla_decay_desc *d, bool transposed) {
@@ -459,33 +460,36 @@ DPool pool(const float *p, const int *idx, int slots, const gla_decay_desc *d, b
                transposed ? (long)d->dv : 1};
 }
 
-// Segments per sequence and chunks per segment of a walk.
-// Splitting reads y and z twice and passes states through memory, so a walk is split only
-// while it leaves SMs idle, and into segments of at least kMinChunks chunks.
-int most_segments(const gla_decay_desc *d, int max_len, int chunk, int V) {
-  constexpr int kMinChunks = 4;
+// Segments per sequence and chunks per segment of a walk.  Splitting reads y and z twice and
+// passes states through memory, so a walk is split only while it leaves SMs idle (148 of
+// them, one CTA a segment and 64 columns).  On tensor cores a chunk of the first pass takes
+// half the time of one of the second: two segments lose up to 128 channels (4 x 8 heads of
+// 2048 tokens of 128 x 128: 46 us instead of 43) and win above (2 x 4 heads of 16384 of
+// 256 x 512: 386 instead of 533), and segments shorter than four chunks do not pay.  On CUDA
+// cores every split pays (3 x 4 heads of 700 tokens of 64 x 64 in fp32: 148 us whole, 34 by chunks).
+int most_segments(const gla_decay_desc *d, int max_len, int chunk, int V, int min_chunks, int least) {
   const long lines = (long)d->B * d->H * ((V + kBV - 1) / kBV);
   const int n = (max_len + chunk - 1) / chunk;
   long p = d->segments ? d->segments : 148 / lines;
-  if (!d->segments && p > n / kMinChunks) p = n / kMinChunks;
+  if (!d->segments && p > n / min_chunks) p = n / min_chunks;
   if (p > kMaxSegments) p = kMaxSegments;
   if (p > n) p = n;
-  return p < 1 ? 1 : (int)p;
+  return p < 1 || (!d->segments && p < least) ? 1 : (int)p;
 }
-void plan_segments(const gla_decay_desc *d, int max_len, int chunk, int V, int *P, int *L) {
-  const int p = most_segments(d, max_len, chunk, V), n = (max_len + chunk - 1) / chunk;
+void plan_segments(const gla_decay_desc *d, int max_len, bool tc, int chunk, int K, int V, int *P, int *L) {
+  const int p = tc ? most_segments(d, max_len, chunk, V, 4, K <= 128 ? 3 : 2) : most_segments(d, max_len, chunk, V, 1, 2);
+  const int n = (max_len + chunk - 1) / chunk;
   *L = (n + p - 1) / p;
   *P = (n + *L - 1) / *L;
 }
 
-// bytes of ws: the state copies of the walk that needs most
+// bytes of ws: the state copies of the walk that needs most, whatever path it takes
 size_t ws_states(const gla_decay_desc *d) {
   int most = 1;
-  for (int V : {d->dk, d->dv})
-    for (int chunk : {32, 64, 128}) {
-      const int p = most_segments(d, d->max_len ? d->max_len : d->T, chunk, V);
-      if (p > most) most = p;
-    }
+  for (int V : {d->dk, d->dv}) {
+    const int p = most_segments(d, d->max_len ? d->max_len : d->T, 32, V, 1, 2);
+    if (p > most) most = p;
+  }
   return most > 1 ? align_up((size_t)d->B * d->H * most * d->dk * d->dv * sizeof(float), 256) : 0;
 }
 // partial outputs of a backward whose contraction over dv is taken in pieces
@@ -516,7 +520,7 @@ int run_walk(DecayWalk w, const gla_decay_desc *d, cudaStream_t st) {
     w.acc_in = k0 > 0;
     w.acc_out = k0 + kPiece < K;
     const int chunk = tc ? decay_chunk_tc() : decay_chunk_cc(w.K);
-    plan_segments(d, w.max_len, chunk, w.V, &w.P, &w.L);
+    plan_segments(d, w.max_len, tc, chunk, w.K, w.V, &w.P, &w.L);
     GLA_TRY(tc ? decay_walk_tc(w, st) : decay_walk_cc(w, d->dtype, st));
   }
   return GLA_OK;
@@ -539,7 +543,7 @@ DecayWalk walk_base(const gla_decay_desc *d, const float *log_decay, const int *
 
 int check_lengths(const gla_decay_desc *d, const int *cu) {
   if ((cu != nullptr) != (d->max_len > 0)) return GLA_ERR_INVALID_ARG;
-  return (uintptr_t)cu & 3u ? GLA_ERR_MISALIGNED : GLA_OK;
+  return check_words(cu);
 }
 
 }  // namespace
@@ -564,6 +568,7 @@ int gla_decay_fwd(const gla_decay_desc *desc, const gla_view *q, const gla_view 
   if (h_final && (desc->slots1 < 1 || (!h_final_index && desc->slots1 < desc->B))) return GLA_ERR_INVALID_ARG;
   GLA_TRY(check_states(h0));
   GLA_TRY(check_states(h_final));
+  for (const void *p : {(const void *)log_decay, (const void *)h0_index, (const void *)h_final_index}) GLA_TRY(check_words(p));
   GLA_TRY(check_ws(desc, false));
   DecayWalk w = walk_base(desc, log_decay, cu_seqlens);
   GLA_TRY(check_view(q, desc->dtype, &w.x));
@@ -585,6 +590,7 @@ int gla_decay_bwd(const gla_decay_desc *desc, const gla_view *q, const gla_view 
   GLA_TRY(check_desc(desc));
   GLA_TRY(check_lengths(desc, cu_seqlens));
   if (!log_decay) return GLA_ERR_INVALID_ARG;
+  GLA_TRY(check_words(log_decay));
   for (const float *s : {h0, dh_final, (const float *)dh0}) GLA_TRY(check_states(s));
   GLA_TRY(check_ws(desc, true));
   DView vq, vk, vv, vdo, vdq, vdk, vdv;
@@ -628,6 +634,8 @@ int gla_decay_step(const gla_decay_desc *desc, const gla_view *q, const gla_view
   GLA_TRY(check_desc(&d));
   if (!log_decay || !state || d.slots1 < 1 || (!index && d.slots1 < d.B)) return GLA_ERR_INVALID_ARG;
   GLA_TRY(check_states(state));
+  GLA_TRY(check_words(log_decay));
+  GLA_TRY(check_words(index));
   if ((uintptr_t)d.workspace & 3u) return GLA_ERR_MISALIGNED;
   DView vq, vk, vv, vo;
   GLA_TRY(check_view(q, d.dtype, &vq));

@@ -329,7 +329,8 @@ int gla_state_scan(const gla_desc *desc, int nseg, int seg, int reverse, const f
  *   for a log_decay that is positive or NaN, taken as 0).  Calls that share a
  *   workspace must not overlap on the GPU.
  *
- * gla_decay_fwd: o and, where h_final is given, the states after each sequence.
+ * gla_decay_fwd: o (overlapping no input) and, where h_final is given, the states after each
+ *   sequence.
  *   h0 [slots0,H,dk,dv] fp32 or NULL (zero states); sequence b starts from entry
  *   h0_index[b] (int32 on the device; NULL: entry b; negative: a zero state).
  *   h_final [slots1,H,dk,dv] or NULL; its entry h_final_index[b] receives sequence b's
@@ -343,7 +344,7 @@ int gla_state_scan(const gla_desc *desc, int nseg, int seg, int reverse, const f
  *   The outputs overlap no input.
  * gla_decay_step: one token for each of B running sequences: the entry index[b] of state
  *   [slots1,H,dk,dv] (NULL: entry b) is updated in place and o reads it.  q, k, v, o by
- *   views (st ignored).  A negative index is a padding row: nothing of it is read and its
+ *   views (st ignored).  o overlaps no input.  A negative index is a padding row: nothing of it is read and its
  *   row of o is left as it was.  So is the later of two rows with one index, and one past the pool
  *   (both reported).  Only B, H, dk, dv, dtype, slots1 and the workspace's status word are used; the
  *   workspace may be NULL (nothing is reported).

@@ -93,7 +93,8 @@ def test_bad_arguments_enqueue_nothing(lib):
     assert lib.gla_decay_fwd(None, v, v, v, a, None, None, None, v, None, None, None) == ARG
     assert fwd(desc(), q=None) == ARG and fwd(desc(), q=vw(0)) == ARG and fwd(desc(), o=vw(st=-1)) == ARG
     assert fwd(desc(), q=vw(4097)) == MIS
-    assert fwd(desc(), ld=None) == ARG
+    assert fwd(desc(), ld=None) == ARG and fwd(desc(), ld=mis) == MIS
+    assert fwd(desc(), h0=a, i0=mis) == MIS and fwd(desc(), hT=a, i1=mis) == MIS
     assert fwd(desc(), cu=a) == ARG and fwd(desc(max_len=5)) == ARG       # cu_seqlens and max_len go together
     assert fwd(desc(max_len=5), cu=mis) == MIS
     assert fwd(desc(), i0=a) == ARG and fwd(desc(), i1=a) == ARG          # an index without its pool
@@ -111,7 +112,7 @@ def test_bad_arguments_enqueue_nothing(lib):
     def bwd(d, do=v, dq=v, ld=a, dh=None, dh0=None):
         return lib.gla_decay_bwd(ctypes.byref(d), v, v, v, ld, None, None, do, dh, dq, v, v, dh0, None)
 
-    assert bwd(desc(), do=None) == ARG and bwd(desc(), dq=vw(0)) == ARG and bwd(desc(), ld=None) == ARG
+    assert bwd(desc(), do=None) == ARG and bwd(desc(), dq=vw(0)) == ARG and bwd(desc(), ld=None) == ARG and bwd(desc(), ld=mis) == MIS
     assert bwd(desc(), dh=mis) == MIS and bwd(desc(), dh0=mis) == MIS
     wide = desc(dv=512)
     wide.workspace_bytes = lib.gla_decay_workspace_size(ctypes.byref(wide), 0)
@@ -122,6 +123,7 @@ def test_bad_arguments_enqueue_nothing(lib):
 
     assert lib.gla_decay_step(None, v, v, v, a, a, None, v, None) == ARG
     assert step(desc(), q=None) == ARG and step(desc(), ld=None) == ARG and step(desc(), state=None) == ARG
+    assert step(desc(), ld=mis) == MIS and step(desc(), index=mis) == MIS
     assert step(desc(), state=mis) == MIS and step(desc(slots1=1)) == ARG and step(desc(slots1=0), index=a) == ARG
 
 
