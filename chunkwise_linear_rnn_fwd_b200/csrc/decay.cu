@@ -46,24 +46,53 @@ struct CcSmem {
   static constexpr int floats = w + C + 1 + 3;
 };
 
-// rows [0, m) x columns [c0, c0 + n) of a token-strided matrix into [C][stride], zeros around them
-template <typename T, int C>
-__device__ __forceinline__ void load_tile(float *dst, int stride, int width, const T *src, long st, int m, int n) {
-  for (int e = threadIdx.x; e < C * (width / 4); e += kThreads) {
-    const int r = e / (width / 4), c = 4 * (e % (width / 4));
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < m) {
-      const T *p = src + r * st + c;
-      if (c < n) v.x = to_f(p[0]);
-      if (c + 1 < n) v.y = to_f(p[1]);
-      if (c + 2 < n) v.z = to_f(p[2]);
-      if (c + 3 < n) v.w = to_f(p[3]);
+__device__ __forceinline__ float4 load_quad(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
+__device__ __forceinline__ float4 load_quad(const __nv_bfloat16 *p) {
+  const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                     __uint_as_float(u.y & 0xffff0000u));
+}
+
+// whether four values at a time can be loaded: data, distances and width are multiples of four
+template <typename T>
+__device__ __forceinline__ bool quads(const T *p, long st, int n) {
+  return ((uintptr_t)p & (4 * sizeof(T) - 1)) == 0 && st % 4 == 0 && n % 4 == 0;
+}
+
+// Rows [0, m) of n values, st apart, into [C][stride] padded with zeros to C x WIDTH; four
+// loads of a thread are in flight together.
+template <typename T, int C, int WIDTH>
+__device__ __forceinline__ void load_tile(float *dst, int stride, const T *src, long st, int m, int n, bool wide) {
+  constexpr int kRow = WIDTH / 4, kAll = C * kRow, kUnroll = kAll / kThreads < 4 ? kAll / kThreads : 4;
+  static_assert(kAll % (kThreads * kUnroll) == 0, "");
+#pragma unroll 1
+  for (int e0 = threadIdx.x; e0 < kAll; e0 += kThreads * kUnroll) {
+    float4 v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int e = e0 + u * kThreads, r = e / kRow, c = 4 * (e % kRow);
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < m && c < n) {
+        const T *p = src + r * st + c;
+        if (wide) {
+          v[u] = load_quad(p);
+        } else {
+          v[u].x = to_f(p[0]);
+          if (c + 1 < n) v[u].y = to_f(p[1]);
+          if (c + 2 < n) v[u].z = to_f(p[2]);
+          if (c + 3 < n) v[u].w = to_f(p[3]);
+        }
+      }
     }
-    *reinterpret_cast<float4 *>(dst + r * stride + c) = v;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int e = e0 + u * kThreads;
+      *reinterpret_cast<float4 *>(dst + (e / kRow) * stride + 4 * (e % kRow)) = v[u];
+    }
   }
 }
 
-template <typename T, int C, int K, bool OUT>
+template <typename T, int C, int K, bool OUT, bool REV>
 __global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
   using L = CcSmem<C, K>;
   extern __shared__ __align__(16) float sm[];
@@ -123,16 +152,17 @@ __global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
   const T *y = (const T *)w.y.p + sq.b * w.y.sb + h * w.y.sh + sq.row0 * w.y.st;
   const T *z = (const T *)w.z.p + sq.b * w.z.sb + h * w.z.sh + sq.row0 * w.z.st + v0;
   const int nv = min(kBV, w.V - v0);
+  const bool wx = OUT && quads(x, w.x.st, w.K), wy = quads(y, w.y.st, w.K), wz = quads(z, w.z.st, nv);
   const long rows = w.packed ? w.T : (long)w.nseq * w.T;
   const int i_end = min(n, (seg + 1) * w.L);
   for (int i = seg * w.L; i < i_end; ++i) {
-    const int c = w.reverse ? n - 1 - i : i;
+    const int c = REV ? n - 1 - i : i;
     const long t0 = (long)c * C;
     const int m = (int)min((long)C, sq.len - t0);
     __syncthreads();
-    if (OUT) load_tile<T, C>(X, L::KS, K, x + t0 * w.x.st, w.x.st, m, w.K);
-    load_tile<T, C>(Y, L::KS, K, y + t0 * w.y.st, w.y.st, m, w.K);
-    load_tile<T, C>(Z, kBV, kBV, z + t0 * w.z.st, w.z.st, m, nv);
+    if (OUT) load_tile<T, C, K>(X, L::KS, x + t0 * w.x.st, w.x.st, m, w.K, wx);
+    load_tile<T, C, K>(Y, L::KS, y + t0 * w.y.st, w.y.st, m, w.K, wy);
+    load_tile<T, C, kBV>(Z, kBV, z + t0 * w.z.st, w.z.st, m, nv, wz);
     __syncthreads();
     constexpr int R = C / 16;
     if (OUT) {
@@ -151,18 +181,19 @@ __global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
 #pragma unroll
         for (int a = 0; a < R; ++a)
 #pragma unroll
-          for (int d = 0; d < R; ++d) {
-            s[a][d] = fmaf(xv[a].x, yv[d].x, s[a][d]);
-            s[a][d] = fmaf(xv[a].y, yv[d].y, s[a][d]);
-            s[a][d] = fmaf(xv[a].z, yv[d].z, s[a][d]);
-            s[a][d] = fmaf(xv[a].w, yv[d].w, s[a][d]);
-          }
+          for (int d = 0; d < R; ++d)
+            if (REV ? d >= a : d <= a) {  // blocks of 16 x 16 on the diagonal's near side
+              s[a][d] = fmaf(xv[a].x, yv[d].x, s[a][d]);
+              s[a][d] = fmaf(xv[a].y, yv[d].y, s[a][d]);
+              s[a][d] = fmaf(xv[a].z, yv[d].z, s[a][d]);
+              s[a][d] = fmaf(xv[a].w, yv[d].w, s[a][d]);
+            }
       }
 #pragma unroll
       for (int a = 0; a < R; ++a)
 #pragma unroll
         for (int d = 0; d < R; ++d) {
-          const int t = ty + 16 * a, u = tx + 16 * d, g = w.reverse ? u - t : t - u;
+          const int t = ty + 16 * a, u = tx + 16 * d, g = REV ? u - t : t - u;
           Pm[t * L::PS + u] = g >= 0 ? s[a][d] * W[g] : 0.f;
         }
       __syncthreads();
@@ -181,23 +212,26 @@ __global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
           in[a].w = fmaf(q, sv.w, in[a].w);
         }
       }
-#pragma unroll 4
-      for (int u = 0; u < C; ++u) {
-        const float4 zv = *reinterpret_cast<const float4 *>(Z + u * kBV + 4 * tx);
 #pragma unroll
-        for (int a = 0; a < R; ++a) {
-          const float q = Pm[(ty + 16 * a) * L::PS + u];
-          ia[a].x = fmaf(q, zv.x, ia[a].x);
-          ia[a].y = fmaf(q, zv.y, ia[a].y);
-          ia[a].z = fmaf(q, zv.z, ia[a].z);
-          ia[a].w = fmaf(q, zv.w, ia[a].w);
+      for (int d = 0; d < R; ++d)
+#pragma unroll 4
+        for (int u = 16 * d; u < 16 * d + 16; ++u) {
+          const float4 zv = *reinterpret_cast<const float4 *>(Z + u * kBV + 4 * tx);
+#pragma unroll
+          for (int a = 0; a < R; ++a)
+            if (REV ? d >= a : d <= a) {
+              const float q = Pm[(ty + 16 * a) * L::PS + u];
+              ia[a].x = fmaf(q, zv.x, ia[a].x);
+              ia[a].y = fmaf(q, zv.y, ia[a].y);
+              ia[a].z = fmaf(q, zv.z, ia[a].z);
+              ia[a].w = fmaf(q, zv.w, ia[a].w);
+            }
         }
-      }
 #pragma unroll
       for (int a = 0; a < R; ++a) {
         const int t = ty + 16 * a;
         if (t >= m) continue;
-        const float f = W[w.reverse ? m - 1 - t : t + 1];
+        const float f = W[REV ? m - 1 - t : t + 1];
         const float r[4] = {fmaf(f, in[a].x, ia[a].x), fmaf(f, in[a].y, ia[a].y), fmaf(f, in[a].z, ia[a].z),
                             fmaf(f, in[a].w, ia[a].w)};
         T *o = (T *)w.o.p + sq.b * w.o.sb + h * w.o.sh + (sq.row0 + t0 + t) * w.o.st + v0;
@@ -216,7 +250,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
     }
     for (int e = tid; e < C * kBV; e += kThreads) {
       const int u = e / kBV;
-      if (u < m) Z[e] *= W[w.reverse ? u + 1 : m - 1 - u];
+      if (u < m) Z[e] *= W[REV ? u + 1 : m - 1 - u];
     }
     __syncthreads();
     const float dm = W[m];
@@ -274,30 +308,35 @@ __global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
   }
 }
 
-template <typename T, int C, int K>
+template <auto kernel>
+int prepare(int smem) {  // a kernel's shared memory is set once per device
+  static DeviceSlots slots;
+  const int e = per_device(slots, [smem] {
+    const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (r != cudaSuccess) note_cuda_error(r);
+    return r == cudaSuccess ? 1 : -1;
+  });
+  return e == 1 ? GLA_OK : GLA_ERR_CUDA;
+}
+
+template <typename T, int C, int K, bool REV>
 int launch_cc(const DecayWalk &w, cudaStream_t st) {
   const int smem = CcSmem<C, K>::floats * 4;
-  static DeviceSlots slots;  // the kernels' shared memory is set once per device
-  const int ready = per_device(slots, [smem] {
-    cudaError_t e = cudaFuncSetAttribute(k_decay_cc<T, C, K, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k_decay_cc<T, C, K, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) note_cuda_error(e);
-    return e == cudaSuccess ? 1 : -1;
-  });
-  if (ready != 1) return GLA_ERR_CUDA;
   const unsigned gx = (unsigned)((long)w.nseq * w.H * ((w.V + kBV - 1) / kBV));
-  if (w.P > 1)
-    GLA_LAUNCH(K_DECAY_STATES, st, (k_decay_cc<T, C, K, false><<<dim3(gx, w.P - 1), kThreads, smem, st>>>(w)));
-  GLA_LAUNCH(K_DECAY_WALK, st, (k_decay_cc<T, C, K, true><<<dim3(gx, w.P), kThreads, smem, st>>>(w)));
+  if (w.P > 1) {
+    if (const int e = prepare<k_decay_cc<T, C, K, false, REV>>(smem)) return e;
+    GLA_LAUNCH(K_DECAY_STATES, st, (k_decay_cc<T, C, K, false, REV><<<dim3(gx, w.P - 1), kThreads, smem, st>>>(w)));
+  }
+  if (const int e = prepare<k_decay_cc<T, C, K, true, REV>>(smem)) return e;
+  GLA_LAUNCH(K_DECAY_WALK, st, (k_decay_cc<T, C, K, true, REV><<<dim3(gx, w.P), kThreads, smem, st>>>(w)));
   return GLA_OK;
 }
 
-template <typename T>
+template <typename T, bool REV>
 int walk_cc(const DecayWalk &w, cudaStream_t st) {
-  if (w.K <= 64) return launch_cc<T, 64, 64>(w, st);
-  if (w.K <= 128) return launch_cc<T, 64, 128>(w, st);
-  return launch_cc<T, 32, 256>(w, st);
+  if (w.K <= 64) return launch_cc<T, 64, 64, REV>(w, st);
+  if (w.K <= 128) return launch_cc<T, 64, 128, REV>(w, st);
+  return launch_cc<T, 32, 256, REV>(w, st);
 }
 
 // ============================================================================
@@ -419,7 +458,8 @@ int step(const gla_decay_desc &d, const DView &q, const DView &k, const DView &v
 int decay_chunk_cc(int K) { return K <= 128 ? 64 : 32; }
 
 int decay_walk_cc(const DecayWalk &w, int dtype, cudaStream_t st) {
-  return dtype == GLA_DTYPE_BF16 ? walk_cc<__nv_bfloat16>(w, st) : walk_cc<float>(w, st);
+  if (w.reverse) return dtype == GLA_DTYPE_BF16 ? walk_cc<__nv_bfloat16, true>(w, st) : walk_cc<float, true>(w, st);
+  return dtype == GLA_DTYPE_BF16 ? walk_cc<__nv_bfloat16, false>(w, st) : walk_cc<float, false>(w, st);
 }
 
 namespace {
