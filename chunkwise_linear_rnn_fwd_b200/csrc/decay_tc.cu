@@ -384,7 +384,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             if (kk < ks) dev::umma_bf16(tmem + kColSc, x + koff(kk), y + koff(kk), id_sc, kb + kk > 0 ? 1u : 0u);
-          if (KB == 2) dev::umma_commit(&xempty[s]);  // X S came first
           if (kb == KB - 1) dev::umma_commit(scfull);
         }
         __syncwarp();
@@ -397,7 +396,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
         const int s = slot(i, kb);
-        if (KB == 2) ok = ok && wait(&xfull[s], phase(i, kb));
         if (!ok) return;
         dev::tc_fence_after();
         const int ks = ksteps_of(kb);
@@ -406,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             if (kk < ks) dev::umma_bf16(tmem + kColOb, x + koff(kk), dS + mnoff(8 * kb + kk), id_o, kb + kk > 0 ? 1u : 0u);
-          if (KB == 1) dev::umma_commit(&xempty[s]);  // X Y^T came first
+          dev::umma_commit(&xempty[s]);  // X Y^T came first
           if (kb == KB - 1) dev::umma_commit(qsdone);
         }
         __syncwarp();
@@ -416,11 +414,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < nloc && ok; ++i) {
       const uint32_t par = (uint32_t)(i & 1);
       const int ts = (live_of(i) + 15) / 16;  // 16-token steps that hold a live token
-      // With 128 channels X S goes last but one: the state that it reads is made from dS of the
-      // chunk before, and P is ready by then.  With 256 channels it goes first, while the
-      // next Y, which has no second buffer, arrives.
-      if (OUT && KB == 2) inter(i);
+      // X S goes behind dS with 128 channels: the state that it reads is made from dS of the
+      // chunk before, and P is ready by then.  With 256 it goes before dS, so that the next
+      // X, which has no second buffer, arrives while dS is formed.
       if (OUT) scores(i);
+      if (OUT && KB == 2) inter(i);
       ok = ok && wait(zready, par);  // (the warps that arrive there have waited for Z)
       if (ok && i > 0) ok = wait(dsempty, par ^ 1u);
       if (!ok) break;

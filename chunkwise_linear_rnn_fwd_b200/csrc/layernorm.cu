@@ -7,14 +7,16 @@
 // Bound by HBM: the forward reads x and writes y, the backward reads x and dy and writes
 // dx.  A row belongs to a group of G threads that hold it in registers, so it is read once:
 // 16-byte loads where the data, the distance of rows and d allow, pairs of single values
-// otherwise.  A CTA of 512 threads stays for many rows, its groups take them in turn, R at a time.
+// otherwise.  A CTA stays for many rows, its groups take them in turn, R at a time.
 // Forward: up to 64 values a thread, a warp a row up to 2048 bf16 values, so that the sums
-// over a row's threads are a small part.  Backward: 8 values a thread, because each costs
-// two more registers for its columns' sums over all rows, and what hides the latency here is the number of
-// warps: with 32 values a thread, a quarter of the warps, 16384 rows of 1024 took 57 us
-// instead of 37, and rings of prefetched rows in shared memory did not make up for it.  The sums
-// over the threads of a row are formed for R rows together.  The backward leaves one partial
-// sum of dw and db per CTA, which a second kernel adds in a fixed order.
+// over a row's threads are a small part (16384 rows of 2048: 30 us; 35 with 8 values a
+// thread).  Backward: 8 values a thread, because each costs two more registers for its
+// columns' sums over all rows, and what hides the latency here is the number of warps: 24 an
+// SM at 80 registers.  (16384 rows of 1024: with 32 values a thread and 16 warps 57 us instead of
+// 30, and rings of prefetched rows in shared memory did not make up for it; with 32 warps at
+// 64 registers, which spill, 36.)  The sums over the threads of a row are formed for R rows
+// together.  The backward leaves one partial sum of dw and db per CTA, which a second kernel
+// adds in a fixed order.
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -23,8 +25,7 @@
 namespace gla {
 namespace {
 
-// The arithmetic runs on pairs of fp32 values (f32x2: one instruction for two), which halves
-// the instructions: at two bytes a value these kernels were bound by them.
+// The arithmetic runs on pairs of fp32 values (f32x2: one instruction for two).
 using dev::add2;
 using dev::bf16pair;
 using dev::f2;
@@ -127,8 +128,7 @@ __device__ __forceinline__ void weights_of(const float *p, float none, int c, in
   }
 }
 
-constexpr int kLnThreads = 512;
-constexpr int kLnCtas = 296;  // two on each of 148 SMs; also the most partial sums of a backward
+constexpr int kBwdCtas = 444;  // three on each of 148 SMs: the most partial sums of a backward
 
 // Sums of V values (V a power of two up to 8) over a group of G threads, each thread getting
 // all of them.  Within a warp the values halve while the lanes they are summed over double:
@@ -180,15 +180,20 @@ struct LnArgs {
   float *part;                 // [CTAs][2][d]
 };
 
-// CTAs of 512 threads that an SM holds: two while the values of a thread leave room in 64 registers
-template <int VEC, int N, int R, bool BWD>
+// Threads of a CTA, and CTAs that an SM holds: as many as leave a thread the registers for its
+// values (64 when 1024 threads stay, 80 when 768 do).
+template <int G, bool BWD>
+constexpr int threads_of() {
+  return BWD && G <= 256 ? 256 : 512;
+}
+template <int VEC, int N, int G, int R, bool BWD>
 constexpr int ctas_per_sm() {
-  return BWD ? (N * VEC <= 8 ? 2 : 1) : (N * VEC * R <= 16 ? 2 : 1);
+  return BWD ? (N * VEC > 8 ? 1 : G <= 256 ? 3 : 2) : (N * VEC * R <= 16 ? 2 : 1);
 }
 
 template <typename T, int VEC, int N, int G, int R>
-__global__ void __launch_bounds__(kLnThreads, ctas_per_sm<VEC, N, R, false>()) k_ln_fwd(LnArgs a) {
-  constexpr int kGroups = kLnThreads / G, P = Pack<T, VEC>::P;
+__global__ void __launch_bounds__(threads_of<G, false>(), ctas_per_sm<VEC, N, G, R, false>()) k_ln_fwd(LnArgs a) {
+  constexpr int kGroups = threads_of<G, false>() / G, P = Pack<T, VEC>::P;
   // two places in turn: a thread past the barrier of one sum cannot reach the writes of the
   // sum after the next before every thread of its group has passed the next one's barrier
   __shared__ float red[2][kGroups * R * (G / 32)];
@@ -265,13 +270,13 @@ __global__ void __launch_bounds__(kLnThreads, ctas_per_sm<VEC, N, R, false>()) k
 // wide for that, in the partial sum's own place.
 template <int VEC, int N, int G>
 __host__ __device__ constexpr bool sums_in_smem() {
-  return G < kLnThreads && 2 * VEC * N * G * sizeof(float) <= 40 * 1024;
+  return G < threads_of<G, true>() && 2 * VEC * N * G * sizeof(float) <= 40 * 1024;
 }
 
 // Thread t of a group carries its columns' sums of dy x^ and dy over all of its rows.
 template <typename T, int VEC, int N, int G, int R>
-__global__ void __launch_bounds__(kLnThreads, ctas_per_sm<VEC, N, R, true>()) k_ln_bwd(LnArgs a) {
-  constexpr int kGroups = kLnThreads / G, P = Pack<T, VEC>::P;
+__global__ void __launch_bounds__(threads_of<G, true>(), ctas_per_sm<VEC, N, G, R, true>()) k_ln_bwd(LnArgs a) {
+  constexpr int kGroups = threads_of<G, true>() / G, P = Pack<T, VEC>::P;
   __shared__ float red[2][kGroups * 2 * R * (G / 32)];  // in turn, as in the forward: one barrier a round
   extern __shared__ float shared_sums[];                // [2][d] (sums_in_smem)
   const int t = threadIdx.x % G, group = threadIdx.x / G;
@@ -281,7 +286,7 @@ __global__ void __launch_bounds__(kLnThreads, ctas_per_sm<VEC, N, R, true>()) k_
   f2 dw[N * P], db[N * P];
 #pragma unroll
   for (int i = 0; i < N * P; ++i) dw[i] = db[i] = zero;
-  constexpr bool kKeep = N * VEC * R <= 8;  // the weights stay in registers
+  constexpr bool kKeep = N * VEC <= 8;  // the weights stay in registers
   f2 wk[kKeep ? N * P : P];
   if constexpr (kKeep)
 #pragma unroll
@@ -408,15 +413,15 @@ __global__ void __launch_bounds__(1024) k_ln_reduce(int parts, int d, const floa
 template <typename T, int VEC, int N, int G, int R, bool BWD>
 int launch(const LnArgs &a, float *dw, float *db, cudaStream_t st) {
   // rows go to the CTAs first, then to their groups
-  const long rounds = (a.rows + R - 1) / R, most = 148 * ctas_per_sm<VEC, N, R, BWD>();
+  const long rounds = (a.rows + R - 1) / R, most = 148 * ctas_per_sm<VEC, N, G, R, BWD>();
   const unsigned grid = (unsigned)(rounds < most ? rounds : most);
   if constexpr (BWD) {
     const size_t smem = sums_in_smem<VEC, N, G>() && a.part ? (size_t)2 * a.d * sizeof(float) : 0;
-    GLA_LAUNCH(K_LN_BWD, st, (k_ln_bwd<T, VEC, N, G, R><<<grid, kLnThreads, smem, st>>>(a)));
+    GLA_LAUNCH(K_LN_BWD, st, (k_ln_bwd<T, VEC, N, G, R><<<grid, threads_of<G, true>(), smem, st>>>(a)));
     if (a.part)
       GLA_LAUNCH(K_LN_REDUCE, st, (k_ln_reduce<<<(2 * a.d + 31) / 32, 1024, 0, st>>>((int)grid, a.d, a.part, dw, db)));
   } else {
-    GLA_LAUNCH(K_LN_FWD, st, (k_ln_fwd<T, VEC, N, G, R><<<grid, kLnThreads, 0, st>>>(a)));
+    GLA_LAUNCH(K_LN_FWD, st, (k_ln_fwd<T, VEC, N, G, R><<<grid, threads_of<G, false>(), 0, st>>>(a)));
   }
   return GLA_OK;
 }
@@ -425,16 +430,18 @@ int launch(const LnArgs &a, float *dw, float *db, cudaStream_t st) {
 template <typename T, int VEC, int N, int G, int R, bool BWD>
 int rows_of(const LnArgs &a, float *dw, float *db, cudaStream_t st) {
   if constexpr (R > 1)
-    if (a.rows <= (long)kLnCtas * (kLnThreads / G) * R / 2) return launch<T, VEC, N, G, 1, BWD>(a, dw, db, st);
+    if (a.rows <= 148L * ctas_per_sm<VEC, N, G, R, BWD>() * (threads_of<G, BWD>() / G) * R / 2)
+      return launch<T, VEC, N, G, 1, BWD>(a, dw, db, st);
   return launch<T, VEC, N, G, R, BWD>(a, dw, db, st);
 }
 
 // N packs a thread: a warp a row while that suffices (more rows at a time where less does),
-// then 64 to 512 threads a row, then 512 threads with more packs.
+// then more threads a row, then more packs.
 template <typename T, int VEC, bool BWD>
 int run(const LnArgs &a, float *dw, float *db, cudaStream_t st) {
+  constexpr int R = sizeof(T) == 2 ? 2 : 1;
   if constexpr (BWD || VEC == 2) {
-    constexpr int N = 8 / VEC, W = 32 * VEC * N, R = sizeof(T) == 2 ? 2 : 1;
+    constexpr int N = 8 / VEC, W = 32 * VEC * N;
     if (a.d <= W) return rows_of<T, VEC, N, 32, R, BWD>(a, dw, db, st);
     if (a.d <= 2 * W) return rows_of<T, VEC, N, 64, R, BWD>(a, dw, db, st);
     if (a.d <= 4 * W) return rows_of<T, VEC, N, 128, R, BWD>(a, dw, db, st);
@@ -482,7 +489,7 @@ extern "C" {
 
 size_t gla_layernorm_workspace_size(long long rows, int d) {
   if (check(GLA_DTYPE_FP32, rows, d) != GLA_OK) return 0;
-  return align_up((size_t)(rows < kLnCtas ? rows : kLnCtas) * 2 * d * sizeof(float), 256);
+  return align_up((size_t)(rows < kBwdCtas ? rows : kBwdCtas) * 2 * d * sizeof(float), 256);
 }
 
 int gla_layernorm_fwd(int dtype, long long rows, int d, const void *x, long long ldx, const float *w, const float *b,
