@@ -624,7 +624,14 @@ def alloc_decay_workspace(nbytes: int, device) -> torch.Tensor:
     return ws
 
 
-def _decay_setup(lib, q, v, index, cu_seqlens, max_len, slots0, slots1, segments, workspace, for_bwd):
+@functools.lru_cache(maxsize=256)
+def _decay_bytes(B, H, T, max_len, dk, dv, dtype, segments, for_bwd) -> int:
+    """decay_workspace_size without its refusal: an invalid call needs no workspace to be refused."""
+    d = _decay_desc(B, H, T, max_len, dk, dv, dtype, segments=segments)
+    return max(load().gla_decay_workspace_size(ctypes.byref(d), for_bwd), 256)
+
+
+def _decay_setup(q, v, index, cu_seqlens, max_len, slots0, slots1, segments, workspace, for_bwd):
     """(B sequences, cu pointer, descriptor, workspace) of a chunked call.  A workspace the
     caller did not pass lives for this call; nobody reads its status word."""
     B, H, T, dk = q.shape
@@ -642,8 +649,7 @@ def _decay_setup(lib, q, v, index, cu_seqlens, max_len, slots0, slots1, segments
     d = _decay_desc(B, H, T, max_len, dk, v.shape[-1], q.dtype, B if slots0 is None else slots0,
                     B if slots1 is None else slots1, segments, workspace)
     if workspace is None:
-        # an invalid descriptor needs 0 bytes and is refused by the call
-        n = max(lib.gla_decay_workspace_size(ctypes.byref(d), for_bwd), 256)
+        n = _decay_bytes(B, H, T, max_len, dk, v.shape[-1], q.dtype, segments, for_bwd)
         workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
         d.workspace, d.workspace_bytes = workspace.data_ptr(), n
     return B, cu, d, workspace
@@ -671,7 +677,7 @@ def gla_decay_fwd(q, k, v, log_decay, *, cu_seqlens=None, max_len=None, h0=None,
     if h_final is None and h_final_index is not None:
         raise ValueError("h_final_index needs h_final")
     slots0, slots1 = (0 if h0 is None else h0.shape[0]), (None if h_final is None else h_final.shape[0])
-    n, cu, d, workspace = _decay_setup(lib, q, v, index, cu_seqlens, max_len, slots0, slots1, segments, workspace, 0)
+    n, cu, d, workspace = _decay_setup(q, v, index, cu_seqlens, max_len, slots0, slots1, segments, workspace, 0)
     if h_final is None and want_final:
         h_final, slots1 = torch.empty(n, H, dk, dv, dtype=f32, device=q.device), n
     keep, p = _views(dt, index, (q, "q", q.shape), (k, "k", q.shape), (v, "v", (B, H, T, dv)), (o, "o", (B, H, T, dv)))
@@ -695,7 +701,7 @@ def gla_decay_bwd(q, k, v, log_decay, do, *, cu_seqlens=None, max_len=None, h0=N
     B, H, T, K = q.shape
     V = v.shape[-1]
     index, dt, f32 = q.get_device(), q.dtype, torch.float32
-    n, cu, d, workspace = _decay_setup(lib, q, v, index, cu_seqlens, max_len, 0, 0, segments, workspace, 1)
+    n, cu, d, workspace = _decay_setup(q, v, index, cu_seqlens, max_len, 0, 0, segments, workspace, 1)
     dq, dk, dv = (torch.empty_like(like) if t is None else t for t, like in ((dq, q), (dk, k), (dv, v)))
     if dh0 is None and want_dh0:
         dh0 = torch.empty(n, H, K, V, dtype=f32, device=q.device)
@@ -759,15 +765,17 @@ def gla_layernorm_fwd(x, w=None, b=None, *, eps=1e-5, y=None, want_stats=True, s
     if code is None:
         raise ValueError(f"unsupported dtype {x.dtype}")
     n = shape[-1]
+    rows = x.numel() // max(1, n)
     if y is None:
-        y = torch.empty(shape, dtype=x.dtype, device=x.device)
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
     mean = rstd = pm = pr = None
     if want_stats:
-        mean = torch.empty(shape[:-1], dtype=f32, device=x.device)
-        rstd = torch.empty(shape[:-1], dtype=f32, device=x.device)
+        mean = torch.empty(rows, dtype=f32, device=x.device)
+        mean = mean if len(shape) == 2 else mean.view(shape[:-1])
+        rstd = torch.empty_like(mean)
         pm, pr = mean.data_ptr(), rstd.data_ptr()
     (px, ldx), (py, ldy) = _row_view(x, "x", x, index), _row_view(y, "y", x, index)
-    r = load().gla_layernorm_fwd(code, x.numel() // max(1, n), n, px, ldx, _dense(w, "w", f32, (n,), index),
+    r = load().gla_layernorm_fwd(code, rows, n, px, ldx, _dense(w, "w", f32, (n,), index),
                                  _dense(b, "b", f32, (n,), index), eps, py, ldy, pm, pr, _raw_stream(stream, index))
     if r != GLA_OK:
         raise GLAError(r, "gla_layernorm_fwd")
@@ -785,10 +793,11 @@ def gla_layernorm_bwd(x, dy, mean, rstd, w=None, *, dx=None, want_dwb=True, work
     n = shape[-1]
     rows = x.numel() // max(1, n)
     if dx is None:
-        dx = torch.empty(shape, dtype=x.dtype, device=x.device)
+        dx = torch.empty_like(x, memory_format=torch.contiguous_format)
     dw = db = pw = pb = None
     if want_dwb:
-        dw, db = torch.empty(n, dtype=f32, device=x.device), torch.empty(n, dtype=f32, device=x.device)
+        dw = torch.empty(n, dtype=f32, device=x.device)
+        db = torch.empty_like(dw)
         pw, pb = dw.data_ptr(), db.data_ptr()
         if workspace is None:
             workspace = torch.empty(lib.gla_layernorm_workspace_size(rows, n), dtype=torch.uint8, device=x.device)
