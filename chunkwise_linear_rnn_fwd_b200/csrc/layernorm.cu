@@ -282,6 +282,7 @@ __global__ void __launch_bounds__(threads_of<G, true>(), ctas_per_sm<VEC, N, G, 
   const int t = threadIdx.x % G, group = threadIdx.x / G;
   const float inv = 1.f / (float)a.d;
   const f2 zero = pk(0.f, 0.f);
+  dev::pdl_launch_dependents();
   const long step = (long)gridDim.x * kGroups * R;
   f2 dw[N * P], db[N * P];
 #pragma unroll
@@ -387,9 +388,10 @@ __global__ void __launch_bounds__(threads_of<G, true>(), ctas_per_sm<VEC, N, G, 
 
 // dw, db from the partial sums: a CTA owns 32 of the 2 d columns, warp v adds the partials
 // v, v + 32, .. of its lane's column, then the first warp adds the 32 sums in order.
-__global__ void __launch_bounds__(1024) k_ln_reduce(int parts, int d, const float *__restrict__ part, float *dw,
+__global__ void __launch_bounds__(1024) k_ln_reduce(int parts, int d, const float *part, float *dw,
                                                     float *db) {
   __shared__ float red[32][33];
+  dev::pdl_wait();  // launched while the backward drains: its partial sums are complete from here on
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long c = (long)blockIdx.x * 32 + lane;
   float s = 0.f;
@@ -419,7 +421,9 @@ int launch(const LnArgs &a, float *dw, float *db, cudaStream_t st) {
     const size_t smem = sums_in_smem<VEC, N, G>() && a.part ? (size_t)2 * a.d * sizeof(float) : 0;
     GLA_LAUNCH(K_LN_BWD, st, (k_ln_bwd<T, VEC, N, G, R><<<grid, threads_of<G, true>(), smem, st>>>(a)));
     if (a.part)
-      GLA_LAUNCH(K_LN_REDUCE, st, (k_ln_reduce<<<(2 * a.d + 31) / 32, 1024, 0, st>>>((int)grid, a.d, a.part, dw, db)));
+      GLA_LAUNCH(K_LN_REDUCE, st,
+                 (void)launch_pdl(k_ln_reduce, dim3((2 * a.d + 31) / 32), dim3(1024), 0, st, (int)grid, a.d,
+                                  (const float *)a.part, dw, db));
   } else {
     GLA_LAUNCH(K_LN_FWD, st, (k_ln_fwd<T, VEC, N, G, R><<<grid, threads_of<G, false>(), 0, st>>>(a)));
   }
