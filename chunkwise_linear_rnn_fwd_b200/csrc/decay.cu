@@ -491,6 +491,12 @@ int check_view(const gla_view *v, int dtype, DView *out) {
   return GLA_OK;
 }
 
+// an output: tokens, heads and sequences (one, if packed) that do not share their rows
+int check_out(const gla_view *v, const gla_decay_desc *d, DView *out) {
+  if (v && ((d->T > 1 && !v->st) || (d->H > 1 && !v->sh) || (d->B > 1 && !d->max_len && !v->sb))) return GLA_ERR_INVALID_ARG;
+  return check_view(v, d->dtype, out);
+}
+
 int check_words(const void *p) { return (uintptr_t)p & 3u ? GLA_ERR_MISALIGNED : GLA_OK; }
 int check_states(const float *p) { return ((uintptr_t)p & 15u) ? GLA_ERR_MISALIGNED : GLA_OK; }
 
@@ -614,7 +620,7 @@ int gla_decay_fwd(const gla_decay_desc *desc, const gla_view *q, const gla_view 
   GLA_TRY(check_view(q, desc->dtype, &w.x));
   GLA_TRY(check_view(k, desc->dtype, &w.y));
   GLA_TRY(check_view(v, desc->dtype, &w.z));
-  GLA_TRY(check_view(o, desc->dtype, &w.o));
+  GLA_TRY(check_out(o, desc, &w.o));
   w.K = desc->dk;
   w.V = desc->dv;
   w.s0 = pool(h0, h0_index, desc->slots0, desc, false);
@@ -638,9 +644,9 @@ int gla_decay_bwd(const gla_decay_desc *desc, const gla_view *q, const gla_view 
   GLA_TRY(check_view(k, desc->dtype, &vk));
   GLA_TRY(check_view(v, desc->dtype, &vv));
   GLA_TRY(check_view(do_, desc->dtype, &vdo));
-  GLA_TRY(check_view(dq, desc->dtype, &vdq));
-  GLA_TRY(check_view(dk, desc->dtype, &vdk));
-  GLA_TRY(check_view(dv, desc->dtype, &vdv));
+  GLA_TRY(check_out(dq, desc, &vdq));
+  GLA_TRY(check_out(dk, desc, &vdk));
+  GLA_TRY(check_out(dv, desc, &vdv));
   cudaStream_t st = (cudaStream_t)stream;
   const DecayWalk base = walk_base(desc, log_decay, cu_seqlens);
   const int B = desc->B;
@@ -681,7 +687,7 @@ int gla_decay_step(const gla_decay_desc *desc, const gla_view *q, const gla_view
   GLA_TRY(check_view(q, d.dtype, &vq));
   GLA_TRY(check_view(k, d.dtype, &vk));
   GLA_TRY(check_view(v, d.dtype, &vv));
-  GLA_TRY(check_view(o, d.dtype, &vo));
+  GLA_TRY(check_out(o, &d, &vo));
   const DPool s = pool(state, index, d.slots1, &d, false);
   cudaStream_t st = (cudaStream_t)stream;
   return d.dtype == GLA_DTYPE_BF16 ? step<__nv_bfloat16>(d, vq, vk, vv, vo, log_decay, s, st)

@@ -8,14 +8,15 @@
 // factor exceeds one.
 //
 // One CTA per (64 columns of V, segment, sequence and head) and one CTA per SM, 16 warps:
-//   warp 0     TMA loads of X, Y, Z into rings
-//   warp 1     issues the products: X Y^T, X S and P Z (M = tokens, two accumulators: the
-//              row factor f meets X S only), dS = Y^T Zw (M = channels)
+//   warps 0-3  one issues the TMA loads of X, Y, Z into rings; one the products: X Y^T, X S
+//              and P Z (M = tokens, two accumulators: the row factor f meets X S only) and
+//              dS = Y^T Zw (M = channels); two help with the scores' far blocks
 //   warps 4-7  scores from TMEM, times D, to bf16 in TMEM (over the scores, as the A operand
 //              of P Z); later O from TMEM to global memory, a 128-byte row per thread
 //   warps 8-.. one thread per state row (channel): S in fp32 registers, dS from TMEM added,
 //              a bf16 copy to shared memory as the B operand of the next chunk's X S
-//   the rest   w (.) Z as a sum of three bf16 tiles (see below)
+//   warps 12-  w (.) Z as a sum of three bf16 tiles (see below); with 256 channels, where
+//              these warps hold the state's second half, the helpers form it
 // The products are issued by one thread of a converged warp from descriptors that differ by
 // constants: formed anew in a loop they took 180 cycles each, longer than the products.
 // The chain from chunk to chunk is dS -> state -> X S, beside it scores -> P -> P Z; the
@@ -33,6 +34,14 @@
 // 64 columns per CTA and not 128: the state and X S shrink, which leaves shared memory for
 // two chunks in flight (one at 256 channels), and a batch of few heads fills twice the SMs.
 // X Y^T is computed again by every 64 columns; X and Y come from L2.
+//
+// Measured: 4 x 37 heads x 2048 tokens of 128 x 128 (two CTAs an SM in turn) 98.9 us: DRAM
+// 37% of its peak, the tensor pipe 36%, the warps issue in 31% of the cycles.  What bounds a
+// chunk is shared memory: the operands of the products (M = 128 by N = 64 reads more bytes a
+// product than any other tile here), TMA's writes and the scaled tiles share 128 bytes a
+// cycle, and a chunk takes 1.4 times as long as that traffic alone.  Unrolled loops of the
+// scaling and of the scores cost more in instruction misses than they save (132 us against
+// 94 at one size); two and three issuing warps were slower than one.
 #include "decay.h"
 #include "tc_common.cuh"
 #include "tc_path.h"
@@ -166,22 +175,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto kblocks_of = [&](int kb) { return max(0, min(2, kblocks - 2 * (kz + kb))); };
   auto slot = [&](int i, int kb) { return (i * KB + kb) & 1; };
   auto phase = [&](int i, int kb) { return (uint32_t)(((i * KB + kb) >> 1) & 1); };
+  // the coordinate along an axis: a tensor shared along it (distance 0) has one entry there
+  auto axis = [](long distance, int c) { return distance ? c : 0; };
   auto load_y = [&](int i, int kb) {
     const int s = slot(i, kb), row = (int)(sq.row0 + (long)chunk_of(i) * kC);
     dev::mbar_arrive_expect_tx(&yfull[s], (uint32_t)(kblocks_of(kb) * kC * 128));
     for (int cb = 0; cb < kblocks_of(kb); ++cb)
-      dev::tma_load_4d(smem + L::y + s * L::kTile + cb * kC * 128, &tmY, 128 * (kz + kb) + cb * 64, row, h, sq.b, &yfull[s]);
+      dev::tma_load_4d(smem + L::y + s * L::kTile + cb * kC * 128, &tmY, 128 * (kz + kb) + cb * 64, row, axis(w.y.sh, h), axis(w.y.sb, sq.b),
+                       &yfull[s]);
   };
   auto load_x = [&](int i, int kb) {
     const int s = slot(i, kb), row = (int)(sq.row0 + (long)chunk_of(i) * kC);
     dev::mbar_arrive_expect_tx(&xfull[s], (uint32_t)(kblocks_of(kb) * kC * 128));
     for (int cb = 0; cb < kblocks_of(kb); ++cb)
-      dev::tma_load_4d(smem + L::x + s * L::kTile + cb * kC * 128, &tmX, 128 * kb + cb * 64, row, h, sq.b, &xfull[s]);
+      dev::tma_load_4d(smem + L::x + s * L::kTile + cb * kC * 128, &tmX, 128 * kb + cb * 64, row, axis(w.x.sh, h), axis(w.x.sb, sq.b),
+                       &xfull[s]);
   };
   auto load_z = [&](int i) {
     const int s = i % NZ, row = (int)(sq.row0 + (long)chunk_of(i) * kC);
     dev::mbar_arrive_expect_tx(&zfull[s], (uint32_t)L::kZTile);
-    dev::tma_load_4d(smem + L::z + s * L::kZTile, &tmZ, v0, row, h, sq.b, &zfull[s]);
+    dev::tma_load_4d(smem + L::z + s * L::kZTile, &tmZ, v0, row, axis(w.z.sh, h), axis(w.z.sb, sq.b), &zfull[s]);
   };
   if (tid == 0 && nloc > 0) {  // the first chunk's loads run beside the set-up
     for (int kb = 0; kb < KB; ++kb) {
@@ -204,60 +217,60 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int t0 = tid - 32 * kScale0;
   constexpr int kStep = 32 * kScaleWarps, kIter = kC * 8 / kStep;  // 16-byte units per pass, passes
   auto scale_z = [&](int i, bool &ok) {
-      const int s = i % NZ;
-      const int m = live_of(i);
-      if (ok) ok = dev::mbar_wait(&zfull[s], (uint32_t)((i / NZ) & 1), w.status);
-      uint8_t *zt = smem + L::z + s * L::kZTile, *zw = smem + L::zw;
-      // a row is eight 16-byte units; their place in the swizzled row does not matter here
-      if (ok && m == kC) {
-        if (i > 0) ok = dev::mbar_wait(dsfull, (uint32_t)((i - 1) & 1), w.status);
+    const int s = i % NZ;
+    const int m = live_of(i);
+    if (ok) ok = dev::mbar_wait(&zfull[s], (uint32_t)((i / NZ) & 1), w.status);
+    uint8_t *zt = smem + L::z + s * L::kZTile, *zw = smem + L::zw;
+    // a row is eight 16-byte units; their place in the swizzled row does not matter here
+    if (ok && m == kC) {
+      if (i > 0) ok = dev::mbar_wait(dsfull, (uint32_t)((i - 1) & 1), w.status);
 #pragma unroll 1
-        for (int j = 0; j < kIter; j += 2) {
-          const int e = 16 * (t0 + j * kStep), r = (t0 + j * kStep) >> 3;
-          const uint4 u0 = *reinterpret_cast<const uint4 *>(zt + e), u1 = *reinterpret_cast<const uint4 *>(zt + e + 16 * kStep);
-          const float f0 = W[REV ? r + 1 : kC - 1 - r], f1 = W[REV ? r + kStep / 8 + 1 : kC - 1 - kStep / 8 - r];
-          uint4 zh, zm, zl;
-          split3(u0, f0, zh, zm, zl);
-          *reinterpret_cast<uint4 *>(zw + e) = zh;
-          *reinterpret_cast<uint4 *>(zw + L::kZTile + e) = zm;
-          *reinterpret_cast<uint4 *>(zw + 2 * L::kZTile + e) = zl;
-          split3(u1, f1, zh, zm, zl);
-          *reinterpret_cast<uint4 *>(zw + e + 16 * kStep) = zh;
-          *reinterpret_cast<uint4 *>(zw + L::kZTile + e + 16 * kStep) = zm;
-          *reinterpret_cast<uint4 *>(zw + 2 * L::kZTile + e + 16 * kStep) = zl;
-        }
-      } else if (ok) {
-        // Rows behind the sequence hold anything, and zero times it must not be NaN: Y's are
-        // cleared (X Y^T of this chunk waits for it), and so are those of Z that the products read.
-        const int m16 = (m + 15) & ~15;
-        if (i > 0) ok = dev::mbar_wait(dsfull, (uint32_t)((i - 1) & 1), w.status);
-#pragma unroll 1
-        for (int u = t0; u < m16 * 8; u += kStep) {
-          const int r = u >> 3, e = 16 * u;
-          uint4 zh, zm, zl, a = *reinterpret_cast<const uint4 *>(zt + e);
-          if (r >= m) {
-            a = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4 *>(zt + e) = a;
-          }
-          split3(a, W[r < m ? (REV ? r + 1 : m - 1 - r) : 0], zh, zm, zl);
-          *reinterpret_cast<uint4 *>(zw + e) = zh;
-          *reinterpret_cast<uint4 *>(zw + L::kZTile + e) = zm;
-          *reinterpret_cast<uint4 *>(zw + 2 * L::kZTile + e) = zl;
-        }
-        const int dead = (kC - m) * 8;
-        for (int kb = 0; kb < KB; ++kb) {
-          const int sy = slot(i, kb);
-          if (ok) ok = dev::mbar_wait(&yfull[sy], phase(i, kb), w.status);
-          if (!ok) break;
-#pragma unroll 1
-          for (int u = t0; u < dead * kblocks_of(kb); u += kStep)
-            *reinterpret_cast<uint4 *>(smem + L::y + sy * L::kTile + (u / dead) * kC * 128 + m * 128 + (u % dead) * 16) =
-                make_uint4(0, 0, 0, 0);
-        }
+      for (int j = 0; j < kIter; j += 2) {
+        const int e = 16 * (t0 + j * kStep), r = (t0 + j * kStep) >> 3;
+        const uint4 u0 = *reinterpret_cast<const uint4 *>(zt + e), u1 = *reinterpret_cast<const uint4 *>(zt + e + 16 * kStep);
+        const float f0 = W[REV ? r + 1 : kC - 1 - r], f1 = W[REV ? r + kStep / 8 + 1 : kC - 1 - kStep / 8 - r];
+        uint4 zh, zm, zl;
+        split3(u0, f0, zh, zm, zl);
+        *reinterpret_cast<uint4 *>(zw + e) = zh;
+        *reinterpret_cast<uint4 *>(zw + L::kZTile + e) = zm;
+        *reinterpret_cast<uint4 *>(zw + 2 * L::kZTile + e) = zl;
+        split3(u1, f1, zh, zm, zl);
+        *reinterpret_cast<uint4 *>(zw + e + 16 * kStep) = zh;
+        *reinterpret_cast<uint4 *>(zw + L::kZTile + e + 16 * kStep) = zm;
+        *reinterpret_cast<uint4 *>(zw + 2 * L::kZTile + e + 16 * kStep) = zl;
       }
-      dev::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) dev::mbar_arrive(zready);
+    } else if (ok) {
+      // Rows behind the sequence hold anything, and zero times it must not be NaN: Y's are
+      // cleared (X Y^T of this chunk waits for it), and so are those of Z that the products read.
+      const int m16 = (m + 15) & ~15;
+      if (i > 0) ok = dev::mbar_wait(dsfull, (uint32_t)((i - 1) & 1), w.status);
+#pragma unroll 1
+      for (int u = t0; u < m16 * 8; u += kStep) {
+        const int r = u >> 3, e = 16 * u;
+        uint4 zh, zm, zl, a = *reinterpret_cast<const uint4 *>(zt + e);
+        if (r >= m) {
+          a = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4 *>(zt + e) = a;
+        }
+        split3(a, W[r < m ? (REV ? r + 1 : m - 1 - r) : 0], zh, zm, zl);
+        *reinterpret_cast<uint4 *>(zw + e) = zh;
+        *reinterpret_cast<uint4 *>(zw + L::kZTile + e) = zm;
+        *reinterpret_cast<uint4 *>(zw + 2 * L::kZTile + e) = zl;
+      }
+      const int dead = (kC - m) * 8;
+      for (int kb = 0; kb < KB; ++kb) {
+        const int sy = slot(i, kb);
+        if (ok) ok = dev::mbar_wait(&yfull[sy], phase(i, kb), w.status);
+        if (!ok) break;
+#pragma unroll 1
+        for (int u = t0; u < dead * kblocks_of(kb); u += kStep)
+          *reinterpret_cast<uint4 *>(smem + L::y + sy * L::kTile + (u / dead) * kC * 128 + m * 128 + (u % dead) * 16) =
+              make_uint4(0, 0, 0, 0);
+      }
+    }
+    dev::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) dev::mbar_arrive(zready);
   };
 
   // ============================ P ============================
@@ -310,164 +323,164 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     set_regs<R::roles>();
     if (warp == kLoadWarp) {
-    // ============================ loads ============================
-    if (lane == 0 && nloc > 0) {
-      bool ok = true;
-      // the next tile of each kind that has not been issued: (chunk, block)
-      int ni = 1;  // chunks 0 .. ni - 1 are issued
-      int xl = KB, yl = KB, zl = 1;
-      for (; ni < nloc && ok; ++ni) {
-        for (int kb = 0; kb < KB && ok; ++kb) {
-          const int s = slot(ni, kb);
-          if (OUT) {
-            if (ni * KB + kb >= 2) ok = dev::mbar_wait(&xempty[s], phase(ni, kb) ^ 1u, w.status);
-            if (!ok) break;
-            load_x(ni, kb);
-            ++xl;
-          }
-        }
-        for (int kb = 0; kb < KB && ok; ++kb) {
-          const int s = slot(ni, kb);
-          if (ni * KB + kb >= 2) ok = dev::mbar_wait(&yempty[s], phase(ni, kb) ^ 1u, w.status);
-          if (!ok) break;
-          load_y(ni, kb);
-          ++yl;
-        }
-        if (ok && ni >= NZ) ok = dev::mbar_wait(&zempty[ni % NZ], (uint32_t)((ni / NZ - 1) & 1), w.status);
-        if (!ok) break;
-        load_z(ni);
-        ++zl;
-      }
-      // every load issued lands before the CTA ends, also where a wait ran out
-      for (int j = max(0, yl - 2); j < yl; ++j) (void)dev::mbar_wait(&yfull[j & 1], (uint32_t)((j >> 1) & 1), w.status);
-      if (OUT)
-        for (int j = max(0, xl - 2); j < xl; ++j) (void)dev::mbar_wait(&xfull[j & 1], (uint32_t)((j >> 1) & 1), w.status);
-      for (int j = max(0, zl - NZ); j < zl; ++j) (void)dev::mbar_wait(&zfull[j % NZ], (uint32_t)((j / NZ) & 1), w.status);
-    }
-    } else if (warp == kIssueWarp) {
-    // ============================ products ============================
-    // the whole warp runs the loop (all of it is warp-uniform), one thread issues
-    constexpr uint32_t id_sc = dev::idesc_bf16(kC, kC, false, false);   // X, Y: K-major
-    constexpr uint32_t id_o = dev::idesc_bf16(kC, kBV, false, true);    // X or P (TMEM); S or Z: MN-major
-    constexpr uint32_t id_dh = dev::idesc_bf16(128, (KB == 1 ? 3 : 2) * kBV, true, true);  // Y, parts of Zw: MN-major
-    constexpr uint32_t id_dl = dev::idesc_bf16(128, kBV, true, true);
-    // descriptors of a tile's first step; step kk lies koff(kk) (K-major) or mnoff(kk) further
-    const uint64_t dX = dev::desc_kmajor(dev::smem_u32(smem + L::x), kC, 0, 0),
-                   dYk = dev::desc_kmajor(dev::smem_u32(smem + L::y), kC, 0, 0),
-                   dYm = dev::desc_mnmajor(dev::smem_u32(smem + L::y), kC, 0, 0),
-                   dZ = dev::desc_mnmajor(dev::smem_u32(smem + L::z), kC, 0, 0),
-                   dS = dev::desc_mnmajor(dev::smem_u32(smem + L::s), 128 * KB, 0, 0),
-                   dZw = dev::desc_mnmajor(dev::smem_u32(smem + L::zw), kC, 0, 0);
-    constexpr auto koff = [](int kk) { return (uint64_t)(((kk >> 2) * kC * 128 + (kk & 3) * 32) >> 4); };
-    constexpr auto mnoff = [](int kk) { return (uint64_t)((kk * 16 * 128) >> 4); };
-    constexpr uint64_t kTileD = L::kTile >> 4, kZTileD = L::kZTile >> 4;
-    const bool leader = dev::elect_one();
-    auto wait = [&](uint64_t *bar, uint32_t par) { return __all_sync(0xffffffffu, dev::mbar_wait(bar, par, w.status)) != 0; };
-    bool ok = true;
-    // The first tiles of chunk i are looked at before the wait for P of the chunk before, so
-    // that X Y^T follows P Z without a pause.
-    auto tiles_of = [&](int i) {
-      ok = ok && wait(&xfull[slot(i, 0)], phase(i, 0)) && wait(&yfull[slot(i, 0)], phase(i, 0));
-    };
-    // X Y^T of chunk i
-    auto scores = [&](int i) {
-      if (live_of(i) < kC) ok = ok && wait(zready, (uint32_t)(i & 1));  // Y's rows behind the sequence are cleared
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        const int s = slot(i, kb);
-        if (KB == 2) ok = ok && wait(&xfull[s], phase(i, kb)) && wait(&yfull[s], phase(i, kb));
-        if (!ok) return;
-        dev::tc_fence_after();
-        const int ks = ksteps_of(kb);
-        const uint64_t x = dX + s * kTileD, y = dYk + s * kTileD;
-        if (leader) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            if (kk < ks) dev::umma_bf16(tmem + kColSc, x + koff(kk), y + koff(kk), id_sc, kb + kk > 0 ? 1u : 0u);
-          if (kb == KB - 1) dev::umma_commit(scfull);
-        }
-        __syncwarp();
-      }
-    };
-    // X S of chunk i
-    auto inter = [&](int i) {
-      ok = ok && wait(sfull, (uint32_t)(i & 1));
-      if (ok && i > 0) ok = wait(oempty, (uint32_t)((i & 1) ^ 1));
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        const int s = slot(i, kb);
-        if (!ok) return;
-        dev::tc_fence_after();
-        const int ks = ksteps_of(kb);
-        const uint64_t x = dX + s * kTileD;
-        if (leader) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            if (kk < ks) dev::umma_bf16(tmem + kColOb, x + koff(kk), dS + mnoff(8 * kb + kk), id_o, kb + kk > 0 ? 1u : 0u);
-          dev::umma_commit(&xempty[s]);  // X Y^T came first
-          if (kb == KB - 1) dev::umma_commit(qsdone);
-        }
-        __syncwarp();
-      }
-    };
-    if (OUT && KB == 1 && nloc > 0) tiles_of(0);
-    for (int i = 0; i < nloc && ok; ++i) {
-      const uint32_t par = (uint32_t)(i & 1);
-      const int ts = (live_of(i) + 15) / 16;  // 16-token steps that hold a live token
-      // X S goes behind dS with 128 channels: the state that it reads is made from dS of the
-      // chunk before, and P is ready by then.  With 256 it goes before dS, so that the next
-      // X, which has no second buffer, arrives while dS is formed.
-      if (OUT) scores(i);
-      if (OUT && KB == 2) inter(i);
-      ok = ok && wait(zready, par);  // (the warps that arrive there have waited for Z)
-      if (ok && i > 0) ok = wait(dsempty, par ^ 1u);
-      if (!ok) break;
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        const int s = slot(i, kb);
-        if (!OUT) ok = ok && wait(&yfull[s], phase(i, kb));
-        if (!ok) break;
-        dev::tc_fence_after();
-        const uint64_t y = dYm + s * kTileD;
-        const uint32_t d = tmem + kColDs + kb * 128;
-        if (leader) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            if (kk < ts) {
-              dev::umma_bf16(d, y + mnoff(kk), dZw + mnoff(kk), id_dh, kk > 0 ? 1u : 0u);
-              if (KB == 2) dev::umma_bf16(d + kBV, y + mnoff(kk), dZw + 2 * kZTileD + mnoff(kk), id_dl, 1u);
+      // ============================ loads ============================
+      if (lane == 0 && nloc > 0) {
+        bool ok = true;
+        // the next tile of each kind that has not been issued: (chunk, block)
+        int ni = 1;  // chunks 0 .. ni - 1 are issued
+        int xl = KB, yl = KB, zl = 1;
+        for (; ni < nloc && ok; ++ni) {
+          for (int kb = 0; kb < KB && ok; ++kb) {
+            const int s = slot(ni, kb);
+            if (OUT) {
+              if (ni * KB + kb >= 2) ok = dev::mbar_wait(&xempty[s], phase(ni, kb) ^ 1u, w.status);
+              if (!ok) break;
+              load_x(ni, kb);
+              ++xl;
             }
-          dev::umma_commit(&yempty[s]);
-          if (kb == KB - 1) dev::umma_commit(dsfull);
+          }
+          for (int kb = 0; kb < KB && ok; ++kb) {
+            const int s = slot(ni, kb);
+            if (ni * KB + kb >= 2) ok = dev::mbar_wait(&yempty[s], phase(ni, kb) ^ 1u, w.status);
+            if (!ok) break;
+            load_y(ni, kb);
+            ++yl;
+          }
+          if (ok && ni >= NZ) ok = dev::mbar_wait(&zempty[ni % NZ], (uint32_t)((ni / NZ - 1) & 1), w.status);
+          if (!ok) break;
+          load_z(ni);
+          ++zl;
+        }
+        // every load issued lands before the CTA ends, also where a wait ran out
+        for (int j = max(0, yl - 2); j < yl; ++j) (void)dev::mbar_wait(&yfull[j & 1], (uint32_t)((j >> 1) & 1), w.status);
+        if (OUT)
+          for (int j = max(0, xl - 2); j < xl; ++j) (void)dev::mbar_wait(&xfull[j & 1], (uint32_t)((j >> 1) & 1), w.status);
+        for (int j = max(0, zl - NZ); j < zl; ++j) (void)dev::mbar_wait(&zfull[j % NZ], (uint32_t)((j / NZ) & 1), w.status);
+      }
+    } else if (warp == kIssueWarp) {
+      // ============================ products ============================
+      // the whole warp runs the loop (all of it is warp-uniform), one thread issues
+      constexpr uint32_t id_sc = dev::idesc_bf16(kC, kC, false, false);   // X, Y: K-major
+      constexpr uint32_t id_o = dev::idesc_bf16(kC, kBV, false, true);    // X or P (TMEM); S or Z: MN-major
+      constexpr uint32_t id_dh = dev::idesc_bf16(128, (KB == 1 ? 3 : 2) * kBV, true, true);  // Y, parts of Zw: MN-major
+      constexpr uint32_t id_dl = dev::idesc_bf16(128, kBV, true, true);
+      // descriptors of a tile's first step; step kk lies koff(kk) (K-major) or mnoff(kk) further
+      const uint64_t dX = dev::desc_kmajor(dev::smem_u32(smem + L::x), kC, 0, 0),
+                     dYk = dev::desc_kmajor(dev::smem_u32(smem + L::y), kC, 0, 0),
+                     dYm = dev::desc_mnmajor(dev::smem_u32(smem + L::y), kC, 0, 0),
+                     dZ = dev::desc_mnmajor(dev::smem_u32(smem + L::z), kC, 0, 0),
+                     dS = dev::desc_mnmajor(dev::smem_u32(smem + L::s), 128 * KB, 0, 0),
+                     dZw = dev::desc_mnmajor(dev::smem_u32(smem + L::zw), kC, 0, 0);
+      constexpr auto koff = [](int kk) { return (uint64_t)(((kk >> 2) * kC * 128 + (kk & 3) * 32) >> 4); };
+      constexpr auto mnoff = [](int kk) { return (uint64_t)((kk * 16 * 128) >> 4); };
+      constexpr uint64_t kTileD = L::kTile >> 4, kZTileD = L::kZTile >> 4;
+      const bool leader = dev::elect_one();
+      auto wait = [&](uint64_t *bar, uint32_t par) { return __all_sync(0xffffffffu, dev::mbar_wait(bar, par, w.status)) != 0; };
+      bool ok = true;
+      // The first tiles of chunk i are looked at before the wait for P of the chunk before, so
+      // that X Y^T follows P Z without a pause.
+      auto tiles_of = [&](int i) {
+        ok = ok && wait(&xfull[slot(i, 0)], phase(i, 0)) && wait(&yfull[slot(i, 0)], phase(i, 0));
+      };
+      // X Y^T of chunk i
+      auto scores = [&](int i) {
+        if (live_of(i) < kC) ok = ok && wait(zready, (uint32_t)(i & 1));  // Y's rows behind the sequence are cleared
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          const int s = slot(i, kb);
+          if (KB == 2) ok = ok && wait(&xfull[s], phase(i, kb)) && wait(&yfull[s], phase(i, kb));
+          if (!ok) return;
+          dev::tc_fence_after();
+          const int ks = ksteps_of(kb);
+          const uint64_t x = dX + s * kTileD, y = dYk + s * kTileD;
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              if (kk < ks) dev::umma_bf16(tmem + kColSc, x + koff(kk), y + koff(kk), id_sc, kb + kk > 0 ? 1u : 0u);
+            if (kb == KB - 1) dev::umma_commit(scfull);
+          }
+          __syncwarp();
+        }
+      };
+      // X S of chunk i
+      auto inter = [&](int i) {
+        ok = ok && wait(sfull, (uint32_t)(i & 1));
+        if (ok && i > 0) ok = wait(oempty, (uint32_t)((i & 1) ^ 1));
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          const int s = slot(i, kb);
+          if (!ok) return;
+          dev::tc_fence_after();
+          const int ks = ksteps_of(kb);
+          const uint64_t x = dX + s * kTileD;
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              if (kk < ks) dev::umma_bf16(tmem + kColOb, x + koff(kk), dS + mnoff(8 * kb + kk), id_o, kb + kk > 0 ? 1u : 0u);
+            dev::umma_commit(&xempty[s]);  // X Y^T came first
+            if (kb == KB - 1) dev::umma_commit(qsdone);
+          }
+          __syncwarp();
+        }
+      };
+      if (OUT && KB == 1 && nloc > 0) tiles_of(0);
+      for (int i = 0; i < nloc && ok; ++i) {
+        const uint32_t par = (uint32_t)(i & 1);
+        const int ts = (live_of(i) + 15) / 16;  // 16-token steps that hold a live token
+        // X S goes behind dS with 128 channels: the state that it reads is made from dS of the
+        // chunk before, and P is ready by then.  With 256 it goes before dS, so that the next
+        // X, which has no second buffer, arrives while dS is formed.
+        if (OUT) scores(i);
+        if (OUT && KB == 2) inter(i);
+        ok = ok && wait(zready, par);  // (the warps that arrive there have waited for Z)
+        if (ok && i > 0) ok = wait(dsempty, par ^ 1u);
+        if (!ok) break;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          const int s = slot(i, kb);
+          if (!OUT) ok = ok && wait(&yfull[s], phase(i, kb));
+          if (!ok) break;
+          dev::tc_fence_after();
+          const uint64_t y = dYm + s * kTileD;
+          const uint32_t d = tmem + kColDs + kb * 128;
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              if (kk < ts) {
+                dev::umma_bf16(d, y + mnoff(kk), dZw + mnoff(kk), id_dh, kk > 0 ? 1u : 0u);
+                if (KB == 2) dev::umma_bf16(d + kBV, y + mnoff(kk), dZw + 2 * kZTileD + mnoff(kk), id_dl, 1u);
+              }
+            dev::umma_commit(&yempty[s]);
+            if (kb == KB - 1) dev::umma_commit(dsfull);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (OUT && KB == 1) inter(i);
+        if (!ok) break;
+        if (OUT) {
+          if (KB == 1 && i + 1 < nloc) tiles_of(i + 1);
+          ok = ok && wait(pfull, par);
+          if (!ok) break;
+          dev::tc_fence_after();
+        }
+        if (leader) {
+          const uint64_t z = dZ + (i % NZ) * kZTileD;
+          if (OUT) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              if (kk < ts) dev::umma_bf16_ts(tmem + kColOa, tmem + kColSc + 32 * (kk >> 1) + 8 * (kk & 1), z + mnoff(kk), id_o, kk > 0 ? 1u : 0u);
+            dev::umma_commit(ofull);
+          }
+          dev::umma_commit(&zempty[i % NZ]);
         }
         __syncwarp();
-      }
-      if (!ok) break;
-      if (OUT && KB == 1) inter(i);
-      if (!ok) break;
-      if (OUT) {
-        if (KB == 1 && i + 1 < nloc) tiles_of(i + 1);
-        ok = ok && wait(pfull, par);
-        if (!ok) break;
-        dev::tc_fence_after();
       }
       if (leader) {
-        const uint64_t z = dZ + (i % NZ) * kZTileD;
-        if (OUT) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            if (kk < ts) dev::umma_bf16_ts(tmem + kColOa, tmem + kColSc + 32 * (kk >> 1) + 8 * (kk & 1), z + mnoff(kk), id_o, kk > 0 ? 1u : 0u);
-          dev::umma_commit(ofull);
-        }
-        dev::umma_commit(&zempty[i % NZ]);
+        dev::umma_commit(done);  // all products have completed before TMEM is released
+        (void)dev::mbar_wait(done, 0, w.status);
       }
       __syncwarp();
-    }
-    if (leader) {
-      dev::umma_commit(done);  // all products have completed before TMEM is released
-      (void)dev::mbar_wait(done, 0, w.status);
-    }
-    __syncwarp();
     } else {
       bool ok = true;
       for (int i = 0; i < nloc; ++i) {
@@ -719,18 +732,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------- host
 
 bool ok_view(const DView &v, const DecayWalk &w) {
-  // TMA: 16-byte base and distances, none of them zero where the axis has more than one
-  // element, and below 2^40 bytes
+  // TMA: 16-byte base and distances below 2^40 bytes, that of tokens not zero; heads or
+  // sequences that share a tensor (distance 0) are an axis of one entry
   const bool dense = !w.packed && w.nseq > 1;
-  auto fits = [](long s, bool used) { return !used || (s > 0 && s % 8 == 0 && s < (1L << 38)); };
-  return ((uintptr_t)v.p & 15u) == 0 && fits(v.st, w.T > 1) && fits(v.sh, w.H > 1) && fits(v.sb, dense);
+  auto fits = [](long s, bool used) { return !used || (s % 8 == 0 && s < (1L << 38)); };
+  return ((uintptr_t)v.p & 15u) == 0 && fits(v.st, w.T > 1) && (v.st > 0 || w.T == 1) && fits(v.sh, w.H > 1) &&
+         fits(v.sb, dense);
 }
 
 bool make_map(CUtensorMap *m, const DView &v, const DecayWalk &w, int channels) {
-  const bool dense = !w.packed && w.nseq > 1;
+  const bool heads = w.H > 1 && v.sh, batch = !w.packed && w.nseq > 1 && v.sb;
   auto step = [](long s, bool used) { return (uint64_t)(used ? 2 * s : 16); };
-  const uint64_t dims[4] = {(uint64_t)channels, (uint64_t)w.T, (uint64_t)w.H, (uint64_t)(dense ? w.nseq : 1)};
-  const uint64_t strides[3] = {step(v.st, w.T > 1), step(v.sh, w.H > 1), step(v.sb, dense)};
+  const uint64_t dims[4] = {(uint64_t)channels, (uint64_t)w.T, (uint64_t)(heads ? w.H : 1), (uint64_t)(batch ? w.nseq : 1)};
+  const uint64_t strides[3] = {step(v.st, w.T > 1), step(v.sh, heads), step(v.sb, batch)};
   return tc::map4_bf16(m, v.p, dims, strides, 64, kC);
 }
 

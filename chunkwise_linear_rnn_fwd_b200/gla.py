@@ -662,7 +662,7 @@ def gla_decay_fwd(q, k, v, log_decay, *, cu_seqlens=None, max_len=None, h0=None,
     o_t = q_t S_t, lambda_h = exp(log_decay[h]).  Returns (o, h_final or None).  See include/gla.h.
 
     q, k [B,H,T,dk], v [B,H,T,dv] with any distances between sequences, heads and tokens (a
-    transposed view of token-major rows is fine); log_decay [H] fp32.  Dense: B sequences of T
+    transposed view of token-major rows is fine, and one expanded over heads); log_decay [H] fp32.  Dense: B sequences of T
     tokens.  Packed: cu_seqlens [n+1] int32, B = 1, sequence i owns rows cu[i] .. cu[i+1]-1 and
     none is longer than max_len; rows of no sequence are left as they are in `o`.
     h0 [slots,H,dk,dv] fp32: start states, sequence i from entry h0_index[i] (int32; default i;
@@ -696,6 +696,7 @@ def gla_decay_bwd(q, k, v, log_decay, do, *, cu_seqlens=None, max_len=None, h0=N
                   dv=None, dh0=None, want_dh0=True, segments=0, workspace=None, stream=None):
     """Backward of gla_decay_fwd: (dq, dk, dv, dh0 or None) from do [B,H,T,dv] and dh_final
     [n,H,dk,dv] (None: zero); h0 [n,H,dk,dv] or None, in order.  The decay is a constant.
+    An input expanded over heads or sequences gets a gradient for each: sum them.
     See include/gla.h."""
     lib = load()
     B, H, T, K = q.shape

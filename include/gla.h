@@ -311,7 +311,9 @@ int gla_state_scan(const gla_desc *desc, int nseg, int seg, int reverse, const f
  * decay: gla_fwd / gla_bwd).  The decay has no gradient here.
  *
  * gla_view: data and the distance in elements between sequences (sb), heads (sh) and
- * tokens (st); a token's channels are contiguous.  Every distance is >= 0.
+ * tokens (st); a token's channels are contiguous.  Every distance is >= 0; one of zero is
+ * an input that heads, sequences or tokens share (an output's distances are not zero, and its
+ * rows do not overlap).
  * gla_decay_desc:
  *   dense   (max_len 0, cu_seqlens NULL) B sequences of T tokens each.
  *   packed  (max_len > 0) cu_seqlens [B+1] int32 on the device, not decreasing: sequence b owns the
@@ -321,8 +323,8 @@ int gla_state_scan(const gla_desc *desc, int nseg, int seg, int reverse, const f
  *   slots0, slots1: entries of the pools h0 and h_final (at least 1 where those are given).
  *   segments: pieces a long sequence is split into to fill the GPU; 0 = automatic.
  *   dk <= 256, dv <= 4096, B*H <= 2^20.  bf16 tensors whose data and distances are multiples of 16
- *   bytes, with dk and dv multiples of 8, run on tcgen05 tensor cores; every other call
- *   runs on CUDA cores (fp32 arithmetic).
+ *   bytes, with dk and dv multiples of 8 and tokens of their own, run on tcgen05 tensor cores;
+ *   every other call runs on CUDA cores (fp32 arithmetic).
  *   workspace: 256-byte aligned, gla_decay_workspace_size(desc, for_bwd) bytes.
  *   Its first 4 bytes are the status word: zero them once; calls only set bits, and
  *   gla_poll_status reads and clears them (GLA_ERR_TIMEOUT; GLA_ERR_INDEX; GLA_ERR_GATE_RANGE
@@ -335,19 +337,20 @@ int gla_state_scan(const gla_desc *desc, int nseg, int seg, int reverse, const f
  *   h0_index[b] (int32 on the device; NULL: entry b; negative: a zero state).
  *   h_final [slots1,H,dk,dv] or NULL; its entry h_final_index[b] receives sequence b's
  *   last state (NULL: entry b; negative: not written).  h_final may be h0 (a pool updated
- *   in place) or must not overlap it.  An index past the pool is reported and treated as negative.  An entry may be written by one sequence of a call only, and a
- *   pool updated in place read by that sequence only: of two that write one entry the
- *   first does, one that would read another's entry starts from zero, and both are
- *   reported (GLA_ERR_INDEX).
+ *   in place) or must not overlap it.  An index past the pool is reported and treated as
+ *   negative.  An entry may be written by one sequence of a call only, and a pool updated in
+ *   place read by that sequence only: of two that write one entry the first does, one that
+ *   would read another's entry starts from zero, and both are reported (GLA_ERR_INDEX).
  * gla_decay_bwd: gradients of a loss given do = dL/do and dh_final = dL/dS_T [B,H,dk,dv]
  *   (NULL: zero): dq, dk, dv and, where given, dh0 [B,H,dk,dv].  h0 [B,H,dk,dv] or NULL.
+ *   Where heads share an input, each head's gradient is written: the input's is their sum.
  *   The outputs overlap no input.
  * gla_decay_step: one token for each of B running sequences: the entry index[b] of state
  *   [slots1,H,dk,dv] (NULL: entry b) is updated in place and o reads it.  q, k, v, o by
- *   views (st ignored).  o overlaps no input.  A negative index is a padding row: nothing of it is read and its
- *   row of o is left as it was.  So is the later of two rows with one index, and one past the pool
- *   (both reported).  Only B, H, dk, dv, dtype, slots1 and the workspace's status word are used; the
- *   workspace may be NULL (nothing is reported).
+ *   views (st ignored).  o overlaps no input.  A negative index is a padding row: nothing of
+ *   it is read and its row of o is left as it was.  So is the later of two rows with one
+ *   index, and one past the pool (both reported).  Only B, H, dk, dv, dtype, slots1 and the
+ *   workspace's status word are used; the workspace may be NULL (nothing is reported).
  * A token that is not finite reaches, as in any product of matrices, every output of its
  * chunk of 128 tokens (64 or 32 on CUDA cores) and all later ones of its sequence, and no other sequence.
  * All calls validate their arguments before enqueuing anything and run asynchronously on

@@ -8,8 +8,8 @@ values of all its terms), h = 2^-8 the half step of bf16:
     dot products and of the chain of chunk updates, each off by at most 2^-23 (rounded or
     truncated) of what it adds up: n 2^-23 A.
   bf16 on tensor cores: a term of o passes one operand rounded to bf16, its score or the
-    state it comes from: h (1 + h) A more.  The states take k and v exactly; their weight
-    times v is a sum of two bf16 numbers, off by at most 2^-16 A.
+    state it comes from: h (1 + h) A more.  The states take k and v exactly, and
+    the weight times v as the exact sum of three bf16 numbers.
   an output stored in bf16: h (|r| + the error so far).
 """
 from __future__ import annotations
@@ -69,7 +69,7 @@ def tolerance(name, ref, A, b, tensor_cores, length):
     e = steps(b, b.dk, b.dv, length) * 2.0 ** -23 * A
     state = name in ("h_final", "dh0")
     if tensor_cores:
-        e = e + (2.0 ** -16 * A if state else H8 * (1 + H8) * A)
+        e = e + (0.0 if state else H8 * (1 + H8) * A)
     if b.dtype == torch.bfloat16 and not state:
         e = e + H8 * (np.abs(ref) + e)
     return e + 1e-30

@@ -84,7 +84,7 @@ def test_bad_descriptors(lib, kw, code):
 
 def test_bad_arguments_enqueue_nothing(lib):
     """Each of these is refused by the host; the addresses are never touched."""
-    vw = lambda p=4096, sb=0, sh=64, st=256: ctypes.byref(G.gla_view(p, sb, sh, st))  # noqa: E731
+    vw = lambda p=4096, sb=300 * 256, sh=64, st=256: ctypes.byref(G.gla_view(p, sb, sh, st))  # noqa: E731
     v, a, mis = vw(), ctypes.c_void_p(4096), ctypes.c_void_p(4098)
 
     def fwd(d, q=v, o=v, ld=a, cu=None, h0=None, i0=None, hT=None, i1=None):
@@ -93,6 +93,8 @@ def test_bad_arguments_enqueue_nothing(lib):
     assert lib.gla_decay_fwd(None, v, v, v, a, None, None, None, v, None, None, None) == ARG
     assert fwd(desc(), q=None) == ARG and fwd(desc(), q=vw(0)) == ARG and fwd(desc(), o=vw(st=-1)) == ARG
     assert fwd(desc(), q=vw(4097)) == MIS
+    for shared in (vw(sh=0), vw(st=0), vw(sb=0)):  # an output whose rows lie on one another
+        assert fwd(desc(), o=shared) == ARG
     assert fwd(desc(), ld=None) == ARG and fwd(desc(), ld=mis) == MIS
     assert fwd(desc(), h0=a, i0=mis) == MIS and fwd(desc(), hT=a, i1=mis) == MIS
     assert fwd(desc(), cu=a) == ARG and fwd(desc(max_len=5)) == ARG       # cu_seqlens and max_len go together
@@ -113,6 +115,7 @@ def test_bad_arguments_enqueue_nothing(lib):
         return lib.gla_decay_bwd(ctypes.byref(d), v, v, v, ld, None, None, do, dh, dq, v, v, dh0, None)
 
     assert bwd(desc(), do=None) == ARG and bwd(desc(), dq=vw(0)) == ARG and bwd(desc(), ld=None) == ARG and bwd(desc(), ld=mis) == MIS
+    assert bwd(desc(), dq=vw(sh=0)) == ARG and bwd(desc(), dq=vw(st=0)) == ARG
     assert bwd(desc(), dh=mis) == MIS and bwd(desc(), dh0=mis) == MIS
     wide = desc(dv=512)
     wide.workspace_bytes = lib.gla_decay_workspace_size(ctypes.byref(wide), 0)

@@ -108,6 +108,36 @@ def test_bwd_dense_without_states(dtype):
     check({"dq": rows(dq), "dk": rows(dk), "dv": rows(dv)}, want, b, on_tc(b))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("what", ["heads", "sequences", "tokens"])
+def test_inputs_shared_by_heads_sequences_or_tokens(dtype, packed, what):
+    """An expanded input (distance zero) is the input written out, and each of those that
+    share it gets its own gradient."""
+    if packed and what == "sequences":
+        pytest.skip("packed sequences share no rows")
+    n, H, T = 2, 3, 150
+    b = Batch([T] * n, H, 64, 72, dtype, seed=21)
+    for name in ("k", "v"):
+        x = getattr(b, name).view(n, T, H, -1)
+        x = {"heads": x[:, :, :1], "sequences": x[:1], "tokens": x[:, :1]}[what]
+        setattr(b, name, x.expand(n, T, H, -1).reshape(n * T, H, -1))
+    x = views(b, ("q", "k", "v", "do"), "tokens" if packed else "dense_tokens")
+    axis = {"heads": 1, "sequences": 0, "tokens": 2}[what]
+    if packed and what == "tokens":  # one row for the tokens of both sequences
+        b.k[:], b.v[:] = b.k[:1].clone(), b.v[:1].clone()
+    for name in ("k", "v"):
+        x[name] = (views(b, (name,), "tokens" if packed else "dense_tokens")[name].narrow(axis, 0, 1).expand(x[name].shape))
+        assert x[name].stride(axis) == 0
+    p = packing(b, "tokens" if packed else "dense")
+    o, hT = pkg.gla_decay_fwd(x["q"], x["k"], x["v"], b.ld.cuda(), h0=b.h0.cuda(), **p)
+    dq, dk, dv, dh0 = pkg.gla_decay_bwd(x["q"], x["k"], x["v"], b.ld.cuda(), x["do"], h0=b.h0.cuda(),
+                                        dh_final=b.dh.cuda(), **p)
+    on = on_tc(b) and what != "tokens"
+    check({"o": rows(o), "h_final": hT}, reference(b), b, on)
+    check({"dq": rows(dq), "dk": rows(dk), "dv": rows(dv), "dh0": dh0}, reference(b, bwd=True), b, on)
+
+
 @pytest.mark.parametrize("segments", [1, 4])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_rows_of_nobody(dtype, segments):
