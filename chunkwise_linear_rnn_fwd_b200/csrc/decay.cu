@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
   const dev::DSeq sq = dev::decay_seq(w, b);
   const int n = (sq.len + C - 1) / C, nseg = max(1, (n + w.L - 1) / w.L);
   if (seg >= nseg || (!OUT && seg == nseg - 1)) return;
+  if (OUT && w.lead) dev::pdl_launch_dependents();
   int i0, i1;
   dev::decay_slots(w.s0, w.s1, w.alias, w.nseq, b, OUT ? w.status : nullptr, i0, i1);
   const double rate = dev::decay_rate(__ldg(w.ld + h), w.status);
@@ -306,6 +307,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
         }
       }
   }
+  if (OUT && w.join && blockIdx.x == 0 && blockIdx.y == 0) dev::pdl_wait();
 }
 
 template <auto kernel>
@@ -328,7 +330,11 @@ int launch_cc(const DecayWalk &w, cudaStream_t st) {
     GLA_LAUNCH(K_DECAY_STATES, st, (k_decay_cc<T, C, K, false, REV><<<dim3(gx, w.P - 1), kThreads, smem, st>>>(w)));
   }
   if (const int e = prepare<k_decay_cc<T, C, K, true, REV>>(smem)) return e;
-  GLA_LAUNCH(K_DECAY_WALK, st, (k_decay_cc<T, C, K, true, REV><<<dim3(gx, w.P), kThreads, smem, st>>>(w)));
+  if (w.join)
+    GLA_LAUNCH(K_DECAY_WALK, st,
+               (void)launch_pdl(k_decay_cc<T, C, K, true, REV>, dim3(gx, w.P), dim3(kThreads), smem, st, w));
+  else
+    GLA_LAUNCH(K_DECAY_WALK, st, (k_decay_cc<T, C, K, true, REV><<<dim3(gx, w.P), kThreads, smem, st>>>(w)));
   return GLA_OK;
 }
 
@@ -513,8 +519,8 @@ DPool pool(const float *p, const int *idx, int slots, const gla_decay_desc *d, b
 // 2048 tokens of 128 x 128: 46 us instead of 43) and win above (2 x 4 heads of 16384 of
 // 256 x 512: 386 instead of 533), and segments shorter than four chunks do not pay.  On CUDA
 // cores every split pays (3 x 4 heads of 700 tokens of 64 x 64 in fp32: 148 us whole, 34 by chunks).
-int most_segments(const gla_decay_desc *d, int max_len, int chunk, int V, int min_chunks, int least) {
-  const long lines = (long)d->B * d->H * ((V + kBV - 1) / kBV);
+long lines_of(const gla_decay_desc *d, int V) { return (long)d->B * d->H * ((V + kBV - 1) / kBV); }
+int most_segments(const gla_decay_desc *d, int max_len, int chunk, long lines, int min_chunks, int least) {
   const int n = (max_len + chunk - 1) / chunk;
   long p = d->segments ? d->segments : 148 / lines;
   if (!d->segments && p > n / min_chunks) p = n / min_chunks;
@@ -522,8 +528,11 @@ int most_segments(const gla_decay_desc *d, int max_len, int chunk, int V, int mi
   if (p > n) p = n;
   return p < 1 || (!d->segments && p < least) ? 1 : (int)p;
 }
-void plan_segments(const gla_decay_desc *d, int max_len, bool tc, int chunk, int K, int V, int *P, int *L) {
-  const int p = tc ? most_segments(d, max_len, chunk, V, 4, K <= 128 ? 3 : 2) : most_segments(d, max_len, chunk, V, 1, 2);
+// lines: CTAs of the unsplit walk
+void plan_segments(const gla_decay_desc *d, int max_len, bool tc, int K, long lines, int *P, int *L) {
+  const int chunk = tc ? decay_chunk_tc() : decay_chunk_cc(K);
+  const int p = tc ? most_segments(d, max_len, chunk, lines, 4, K <= 128 ? 3 : 2)
+                   : most_segments(d, max_len, chunk, lines, 1, 2);
   const int n = (max_len + chunk - 1) / chunk;
   *L = (n + p - 1) / p;
   *P = (n + *L - 1) / *L;
@@ -533,7 +542,7 @@ void plan_segments(const gla_decay_desc *d, int max_len, bool tc, int chunk, int
 size_t ws_states(const gla_decay_desc *d) {
   int most = 1;
   for (int V : {d->dk, d->dv}) {
-    const int p = most_segments(d, d->max_len ? d->max_len : d->T, 32, V, 1, 2);
+    const int p = most_segments(d, d->max_len ? d->max_len : d->T, 32, lines_of(d, V), 1, 2);
     if (p > most) most = p;
   }
   return most > 1 ? align_up((size_t)d->B * d->H * most * d->dk * d->dv * sizeof(float), 256) : 0;
@@ -551,8 +560,9 @@ int check_ws(const gla_decay_desc *d, bool bwd) {
   return GLA_OK;
 }
 
-// One walk, its contraction over K channels in pieces of at most kPiece.
-int run_walk(DecayWalk w, const gla_decay_desc *d, cudaStream_t st) {
+// One walk, its contraction over K channels in pieces of at most kPiece.  beside: the CTAs
+// of the walks that run beside it, which are then whole and in one piece (0: it runs alone).
+int run_walk(DecayWalk w, const gla_decay_desc *d, cudaStream_t st, long beside = 0) {
   const int K = w.K;
   const long es = d->dtype == GLA_DTYPE_BF16 ? 2 : 4;
   char *const x = (char *)w.x.p, *const y = (char *)w.y.p;
@@ -565,11 +575,17 @@ int run_walk(DecayWalk w, const gla_decay_desc *d, cudaStream_t st) {
     if (s0) w.s0.p = s0 + k0 * w.s0.row;
     w.acc_in = k0 > 0;
     w.acc_out = k0 + kPiece < K;
-    const int chunk = tc ? decay_chunk_tc() : decay_chunk_cc(w.K);
-    plan_segments(d, w.max_len, tc, chunk, w.K, w.V, &w.P, &w.L);
+    plan_segments(d, w.max_len, tc, w.K, lines_of(d, w.V) + beside, &w.P, &w.L);
     GLA_TRY(tc ? decay_walk_tc(w, st) : decay_walk_cc(w, d->dtype, st));
   }
   return GLA_OK;
+}
+
+// whether a walk stays in one piece and one segment where `lines` CTAs run
+bool whole(const DecayWalk &w, const gla_decay_desc *d, long lines) {
+  int P, L;
+  plan_segments(d, w.max_len, decay_tc_takes(w, d->dtype), w.K, lines, &P, &L);
+  return w.K <= kPiece && P == 1;
 }
 
 DecayWalk walk_base(const gla_decay_desc *d, const float *log_decay, const int *cu) {
@@ -650,24 +666,33 @@ int gla_decay_bwd(const gla_decay_desc *desc, const gla_view *q, const gla_view 
   cudaStream_t st = (cudaStream_t)stream;
   const DecayWalk base = walk_base(desc, log_decay, cu_seqlens);
   const int B = desc->B;
-  DecayWalk w = base;  // dq = do S^T
-  w.K = desc->dv, w.V = desc->dk;
-  w.x = vdo, w.y = vv, w.z = vk, w.o = vdq;
-  w.s0 = pool(h0, nullptr, B, desc, true);
-  GLA_TRY(run_walk(w, desc, st));
-  w = base;  // dk = v R^T
-  w.reverse = 1;
-  w.K = desc->dv, w.V = desc->dk;
-  w.x = vv, w.y = vdo, w.z = vq, w.o = vdk;
-  w.s0 = pool(dh_final, nullptr, B, desc, true);
-  GLA_TRY(run_walk(w, desc, st));
-  w = base;  // dv = k R, dh0 = lambda R_1
-  w.reverse = 1;
-  w.K = desc->dk, w.V = desc->dv;
-  w.x = vk, w.y = vq, w.z = vdo, w.o = vdv;
-  w.s0 = pool(dh_final, nullptr, B, desc, false);
-  w.s1 = pool(dh0, nullptr, B, desc, false);
-  return run_walk(w, desc, st);
+  DecayWalk q_ = base;  // dq = do S^T
+  q_.K = desc->dv, q_.V = desc->dk;
+  q_.x = vdo, q_.y = vv, q_.z = vk, q_.o = vdq;
+  q_.s0 = pool(h0, nullptr, B, desc, true);
+  DecayWalk k_ = base;  // dk = v R^T
+  k_.reverse = 1;
+  k_.K = desc->dv, k_.V = desc->dk;
+  k_.x = vv, k_.y = vdo, k_.z = vq, k_.o = vdk;
+  k_.s0 = pool(dh_final, nullptr, B, desc, true);
+  DecayWalk v_ = base;  // dv = k R, dh0 = lambda R_1
+  v_.reverse = 1;
+  v_.K = desc->dk, v_.V = desc->dv;
+  v_.x = vk, v_.y = vq, v_.z = vdo, v_.o = vdv;
+  v_.s0 = pool(dh_final, nullptr, B, desc, false);
+  v_.s1 = pool(dh0, nullptr, B, desc, false);
+  // The three share nothing but the workspace.  Where together they fill the GPU well enough
+  // to stay whole they use none of it and run side by side.
+  const long all = 2 * lines_of(desc, desc->dk) + lines_of(desc, desc->dv);
+  if (whole(q_, desc, all) && whole(k_, desc, all) && whole(v_, desc, all)) {
+    q_.lead = k_.lead = k_.join = v_.join = 1;
+    GLA_TRY(run_walk(q_, desc, st, all - lines_of(desc, q_.V)));
+    GLA_TRY(run_walk(k_, desc, st, all - lines_of(desc, k_.V)));
+    return run_walk(v_, desc, st, all - lines_of(desc, v_.V));
+  }
+  GLA_TRY(run_walk(q_, desc, st));
+  GLA_TRY(run_walk(k_, desc, st));
+  return run_walk(v_, desc, st);
 }
 
 int gla_decay_step(const gla_decay_desc *desc, const gla_view *q, const gla_view *k, const gla_view *v,

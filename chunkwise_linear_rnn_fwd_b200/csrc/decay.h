@@ -42,6 +42,10 @@ struct DecayWalk {
   float *ws;    // [nseq*H][P][K][V]: entry 0 a copy of the start state, entry s the state after segment s-1
   float *acc;   // [H][rows][V] partial outputs of a contraction taken in pieces (rows: nseq * T, or T packed)
   int acc_in, acc_out;  // add the partial outputs to this walk's; write them instead of o
+  // Walks that need nothing of one another run beside each other: `lead` lets the walk
+  // launched next start once all CTAs of this one have, `join` is that next walk, which then
+  // ends no sooner than this one.
+  int lead, join;
   unsigned *status;
 };
 

@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int n = (sq.len + kC - 1) / kC, nseg = max(1, (n + w.L - 1) / w.L);
   if (seg >= nseg || (!OUT && seg == nseg - 1)) return;  // the whole CTA
+  if (OUT && w.lead) dev::pdl_launch_dependents();
   const int c_begin = seg * w.L, nloc = max(0, min(n, c_begin + w.L) - c_begin);
   auto chunk_of = [&](int i) { return REV ? n - 1 - (c_begin + i) : c_begin + i; };
   auto live_of = [&](int i) { return min(kC, sq.len - chunk_of(i) * kC); };
@@ -727,6 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   dev::tc_fence_before();
   __syncthreads();
   if (warp == kIssueWarp) dev::tmem_dealloc(tmem, kTmemCols);
+  if (OUT && w.join && blockIdx.x == 0 && blockIdx.y == 0) dev::pdl_wait();
 }
 
 // ---------------------------------------------------------------- host
@@ -774,7 +776,11 @@ int launch(const DecayWalk &w, cudaStream_t st) {
   }
   constexpr int smem = Smem<KB>::bytes + 1024;
   if (const int e = prepare<k_decay_tc<KB, true, REV, ACC>>(smem)) return e;
-  GLA_LAUNCH(K_DECAY_WALK, st, (k_decay_tc<KB, true, REV, ACC><<<dim3(gx, w.P), kThreads, smem, st>>>(w, mx, my, mz)));
+  if (w.join)
+    GLA_LAUNCH(K_DECAY_WALK, st,
+               (void)launch_pdl(k_decay_tc<KB, true, REV, ACC>, dim3(gx, w.P), dim3(kThreads), smem, st, w, mx, my, mz));
+  else
+    GLA_LAUNCH(K_DECAY_WALK, st, (k_decay_tc<KB, true, REV, ACC><<<dim3(gx, w.P), kThreads, smem, st>>>(w, mx, my, mz)));
   return GLA_OK;
 }
 

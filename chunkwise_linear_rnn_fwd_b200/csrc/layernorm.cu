@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(threads_of<G, true>(), ctas_per_sm<VEC, N, G, 
   const int t = threadIdx.x % G, group = threadIdx.x / G;
   const float inv = 1.f / (float)a.d;
   const f2 zero = pk(0.f, 0.f);
-  dev::pdl_launch_dependents();
+  if (a.part) dev::pdl_launch_dependents();
   const long step = (long)gridDim.x * kGroups * R;
   f2 dw[N * P], db[N * P];
 #pragma unroll
