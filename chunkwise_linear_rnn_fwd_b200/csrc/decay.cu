@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
   const dev::DSeq sq = dev::decay_seq(w, b);
   const int n = (sq.len + C - 1) / C, nseg = max(1, (n + w.L - 1) / w.L);
   if (seg >= nseg || (!OUT && seg == nseg - 1)) return;
-  if (OUT && w.lead) dev::pdl_launch_dependents();
+  if (!OUT || w.lead) dev::pdl_launch_dependents();
   int i0, i1;
   dev::decay_slots(w.s0, w.s1, w.alias, w.nseq, b, OUT ? w.status : nullptr, i0, i1);
   const double rate = dev::decay_rate(__ldg(w.ld + h), w.status);
@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
   float *wsb = w.ws + bh * w.P * KV;
   const bool pass = w.P > 1 && nseg > 1;  // states come from and go to ws
   const float far = (float)dev::decay_pow(rate, (long)w.L * C);
+  if (OUT && pass) dev::pdl_wait();
 #pragma unroll 1
   for (int i = 0; i < K / 64 + (K % 64 ? 1 : 0); ++i)
 #pragma unroll
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
         }
       }
   }
-  if (OUT && w.join && blockIdx.x == 0 && blockIdx.y == 0) dev::pdl_wait();
+  if (OUT && w.follows() && blockIdx.x == 0 && blockIdx.y == 0) dev::pdl_wait();
 }
 
 template <auto kernel>
@@ -330,7 +331,7 @@ int launch_cc(const DecayWalk &w, cudaStream_t st) {
     GLA_LAUNCH(K_DECAY_STATES, st, (k_decay_cc<T, C, K, false, REV><<<dim3(gx, w.P - 1), kThreads, smem, st>>>(w)));
   }
   if (const int e = prepare<k_decay_cc<T, C, K, true, REV>>(smem)) return e;
-  if (w.join)
+  if (w.follows())
     GLA_LAUNCH(K_DECAY_WALK, st,
                (void)launch_pdl(k_decay_cc<T, C, K, true, REV>, dim3(gx, w.P), dim3(kThreads), smem, st, w));
   else

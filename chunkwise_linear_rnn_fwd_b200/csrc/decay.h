@@ -46,6 +46,11 @@ struct DecayWalk {
   // launched next start once all CTAs of this one have, `join` is that next walk, which then
   // ends no sooner than this one.
   int lead, join;
+  // The walk of a split call starts beside its pre-pass in the same way, and waits for it
+  // before it reads the states of the segments.
+#ifdef __CUDACC__
+  __host__ __device__ __forceinline__ bool follows() const { return join || P > 1; }
+#endif
   unsigned *status;
 };
 

@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int n = (sq.len + kC - 1) / kC, nseg = max(1, (n + w.L - 1) / w.L);
   if (seg >= nseg || (!OUT && seg == nseg - 1)) return;  // the whole CTA
-  if (OUT && w.lead) dev::pdl_launch_dependents();
+  if (!OUT || w.lead) dev::pdl_launch_dependents();
   const int c_begin = seg * w.L, nloc = max(0, min(n, c_begin + w.L) - c_begin);
   auto chunk_of = [&](int i) { return REV ? n - 1 - (c_begin + i) : c_begin + i; };
   auto live_of = [&](int i) { return min(kC, sq.len - chunk_of(i) * kC); };
@@ -610,6 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int e = 0; e < kBV; ++e) S[e] = 0.f;
     if (kok) {
       if (OUT && pass) {
+        dev::pdl_wait();
         // entry 0: the start state (segment 0); entries 1 .. seg: states of the segments before
         const float far = (float)dev::decay_pow(rate, (long)w.L * kC);
         for (int j = seg == 0 ? 0 : 1; j <= seg; ++j) {
@@ -728,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   dev::tc_fence_before();
   __syncthreads();
   if (warp == kIssueWarp) dev::tmem_dealloc(tmem, kTmemCols);
-  if (OUT && w.join && blockIdx.x == 0 && blockIdx.y == 0) dev::pdl_wait();
+  if (OUT && w.follows() && blockIdx.x == 0 && blockIdx.y == 0) dev::pdl_wait();
 }
 
 // ---------------------------------------------------------------- host
@@ -776,7 +777,7 @@ int launch(const DecayWalk &w, cudaStream_t st) {
   }
   constexpr int smem = Smem<KB>::bytes + 1024;
   if (const int e = prepare<k_decay_tc<KB, true, REV, ACC>>(smem)) return e;
-  if (w.join)
+  if (w.follows())
     GLA_LAUNCH(K_DECAY_WALK, st,
                (void)launch_pdl(k_decay_tc<KB, true, REV, ACC>, dim3(gx, w.P), dim3(kThreads), smem, st, w, mx, my, mz));
   else
