@@ -140,14 +140,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tiles = (w.V + kBV - 1) / kBV;
-  const int vt = blockIdx.x % tiles, seg = blockIdx.y;
-  const long bh = blockIdx.x / tiles;
-  const int b = (int)(bh / w.H), h = (int)(bh % w.H), v0 = vt * kBV;
+  const uint32_t line = blockIdx.x / (uint32_t)tiles;
+  const int vt = (int)(blockIdx.x - line * (uint32_t)tiles), seg = blockIdx.y;
+  const long bh = line;
+  const int b = (int)(line / (uint32_t)w.H), h = (int)(line - (uint32_t)b * (uint32_t)w.H), v0 = vt * kBV;
   const int kz = OUT ? 0 : blockIdx.z;  // without outputs, 128 channels a CTA: the first block of these
-  // what the set-up reads from memory is asked for at once
-  const float ld = __ldg(w.ld + h);
-  const dev::DSeq sq = dev::decay_seq(w, b);
-  if (tid == 0) {
+  if (tid == 32 * kLoadWarp) {
     dev::prefetch_tmap(&tmY);
     dev::prefetch_tmap(&tmZ);
     if (OUT) dev::prefetch_tmap(&tmX);
@@ -164,6 +162,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     dev::mbar_init(done, 1);
     dev::fence_mbar_init();
   }
+  // what the set-up reads from memory is asked for at once
+  const float ld = __ldg(w.ld + h);
+  const dev::DSeq sq = dev::decay_seq(w, b);
   const int n = (sq.len + kC - 1) / kC, nseg = max(1, (n + w.L - 1) / w.L);
   if (seg >= nseg || (!OUT && seg == nseg - 1)) return;  // the whole CTA
   if (!OUT || w.lead) dev::pdl_launch_dependents();
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     dev::mbar_arrive_expect_tx(&zfull[s], (uint32_t)L::kZTile);
     dev::tma_load_4d(smem + L::z + s * L::kZTile, &tmZ, v0, row, axis(w.z.sh, h), axis(w.z.sb, sq.b), &zfull[s]);
   };
-  if (tid == 0 && nloc > 0) {  // the first chunk's loads run beside the set-up
+  if (tid == 32 * kLoadWarp && nloc > 0) {  // the first chunk's loads run beside the set-up
     for (int kb = 0; kb < KB; ++kb) {
       if (OUT) load_x(0, kb);
       load_y(0, kb);
