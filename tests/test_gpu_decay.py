@@ -339,6 +339,49 @@ def test_streams_and_graphs():
     check({"o": os, "h_final": state[:1]}, reference(f), f, False)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("segments", [0, 3])
+@pytest.mark.parametrize("graph", [False, True])
+def test_what_follows_finds_the_call_complete(dtype, segments, graph):
+    """Walks of a call start before the kernel ahead of them ends; what the stream does next
+    (outputs copied, inputs, states and workspace overwritten) still comes after all of them."""
+    b = Batch([900, 40, 513], 3, 64, 128, dtype, seed=61)
+    x = views(b, ("q", "k", "v", "do"), "tokens")
+    ld, p, h0, dh = b.ld.cuda(), packing(b, "tokens"), b.h0.cuda(), b.dh.cuda()
+    keep = {n: t.clone() for n, t in x.items()}
+    ws = pkg.alloc_decay_workspace(pkg.decay_workspace_size(3, 3, b.rows, 64, 128, dtype, True, max_len=p["max_len"],
+                                                            segments=segments), "cuda")
+
+    def run():
+        for n in x:
+            x[n].copy_(keep[n])
+        out = []
+        for _ in range(2):
+            o, hT = pkg.gla_decay_fwd(x["q"], x["k"], x["v"], ld, h0=h0, segments=segments, workspace=ws, **p)
+            g = pkg.gla_decay_bwd(x["q"], x["k"], x["v"], ld, x["do"], h0=h0, dh_final=dh, segments=segments,
+                                  workspace=ws, **p)
+            out.append([t.clone() for t in (o, hT, *g)])
+            ws[256:].fill_(255)
+        for t in x.values():
+            t.fill_(float("nan"))
+        return out
+
+    if graph:
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = run()
+        for _ in range(3):
+            g.replay()
+    else:
+        out = run()
+    want, wantg = reference(b), reference(b, bwd=True)
+    for o, hT, dq, dk, dv, dh0 in out:
+        check({"o": rows(o), "h_final": hT}, want, b, on_tc(b))
+        check({"dq": rows(dq), "dk": rows(dk), "dv": rows(dv), "dh0": dh0}, wantg, b, on_tc(b))
+    assert pkg.poll_status(ws) == OK
+
+
 def test_offsets_past_32_bits():
     """A pool and rows whose far end lies more than 2^31 elements from the start."""
     H, d = 1, 64
