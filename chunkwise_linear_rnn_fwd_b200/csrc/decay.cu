@@ -104,7 +104,11 @@ __global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
   const int b = (int)(bh / w.H), h = (int)(bh % w.H), v0 = vt * kBV;
   const dev::DSeq sq = dev::decay_seq(w, b);
   const int n = (sq.len + C - 1) / C, nseg = max(1, (n + w.L - 1) / w.L);
-  if (seg >= nseg || (!OUT && seg == nseg - 1)) return;
+  if (seg >= nseg || (!OUT && seg == nseg - 1)) {
+    if (!OUT && w.pre_join && blockIdx.x == 0 && blockIdx.y == 0) dev::pdl_wait();
+    return;
+  }
+  if (OUT && w.wait_first) dev::pdl_wait();
   if (!OUT || w.lead) dev::pdl_launch_dependents();
   int i0, i1;
   dev::decay_slots(w.s0, w.s1, w.alias, w.nseq, b, OUT ? w.status : nullptr, i0, i1);
@@ -116,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
   float *wsb = w.ws + bh * w.P * KV;
   const bool pass = w.P > 1 && nseg > 1;  // states come from and go to ws
   const float far = (float)dev::decay_pow(rate, (long)w.L * C);
-  if (OUT && pass) dev::pdl_wait();
+  if (OUT && pass && !w.settled) dev::pdl_wait();
 #pragma unroll 1
   for (int i = 0; i < K / 64 + (K % 64 ? 1 : 0); ++i)
 #pragma unroll
@@ -308,7 +312,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
         }
       }
   }
-  if (OUT && w.follows() && blockIdx.x == 0 && blockIdx.y == 0) dev::pdl_wait();
+  if ((OUT ? w.follows() : w.pre_join) && blockIdx.x == 0 && blockIdx.y == 0) dev::pdl_wait();
 }
 
 template <auto kernel>
@@ -326,10 +330,15 @@ template <typename T, int C, int K, bool REV>
 int launch_cc(const DecayWalk &w, cudaStream_t st) {
   const int smem = CcSmem<C, K>::floats * 4;
   const unsigned gx = (unsigned)((long)w.nseq * w.H * ((w.V + kBV - 1) / kBV));
-  if (w.P > 1) {
+  if (w.P > 1 && (w.stage & 1)) {
     if (const int e = prepare<k_decay_cc<T, C, K, false, REV>>(smem)) return e;
-    GLA_LAUNCH(K_DECAY_STATES, st, (k_decay_cc<T, C, K, false, REV><<<dim3(gx, w.P - 1), kThreads, smem, st>>>(w)));
+    if (w.pre_join)
+      GLA_LAUNCH(K_DECAY_STATES, st,
+                 (void)launch_pdl(k_decay_cc<T, C, K, false, REV>, dim3(gx, w.P - 1), dim3(kThreads), smem, st, w));
+    else
+      GLA_LAUNCH(K_DECAY_STATES, st, (k_decay_cc<T, C, K, false, REV><<<dim3(gx, w.P - 1), kThreads, smem, st>>>(w)));
   }
+  if (!(w.stage & 2)) return GLA_OK;
   if (const int e = prepare<k_decay_cc<T, C, K, true, REV>>(smem)) return e;
   if (w.follows())
     GLA_LAUNCH(K_DECAY_WALK, st,
@@ -554,16 +563,20 @@ size_t ws_acc(const gla_decay_desc *d) {
   return d->dv > kPiece ? align_up(rows * d->H * d->dk * sizeof(float), 256) : 0;
 }
 
+// The three walks of a backward, unless they need ws_acc, run together: states for each.
+size_t ws_bytes(const gla_decay_desc *d, bool bwd) {
+  return kStatusBytes + ws_states(d) * (bwd && d->dv <= kPiece ? 3 : 1) + (bwd ? ws_acc(d) : 0);
+}
+
 int check_ws(const gla_decay_desc *d, bool bwd) {
   if (!d->workspace) return GLA_ERR_INVALID_ARG;
   if ((uintptr_t)d->workspace & 255u) return GLA_ERR_MISALIGNED;
-  if (d->workspace_bytes < kStatusBytes + ws_states(d) + (bwd ? ws_acc(d) : 0)) return GLA_ERR_WORKSPACE_TOO_SMALL;
+  if (d->workspace_bytes < ws_bytes(d, bwd)) return GLA_ERR_WORKSPACE_TOO_SMALL;
   return GLA_OK;
 }
 
-// One walk, its contraction over K channels in pieces of at most kPiece.  beside: the CTAs
-// of the walks that run beside it, which are then whole and in one piece (0: it runs alone).
-int run_walk(DecayWalk w, const gla_decay_desc *d, cudaStream_t st, long beside = 0) {
+// One walk by itself, its contraction over K channels in pieces of at most kPiece.
+int run_walk(DecayWalk w, const gla_decay_desc *d, cudaStream_t st) {
   const int K = w.K;
   const long es = d->dtype == GLA_DTYPE_BF16 ? 2 : 4;
   char *const x = (char *)w.x.p, *const y = (char *)w.y.p;
@@ -576,17 +589,37 @@ int run_walk(DecayWalk w, const gla_decay_desc *d, cudaStream_t st, long beside 
     if (s0) w.s0.p = s0 + k0 * w.s0.row;
     w.acc_in = k0 > 0;
     w.acc_out = k0 + kPiece < K;
-    plan_segments(d, w.max_len, tc, w.K, lines_of(d, w.V) + beside, &w.P, &w.L);
+    plan_segments(d, w.max_len, tc, w.K, lines_of(d, w.V), &w.P, &w.L);
     GLA_TRY(tc ? decay_walk_tc(w, st) : decay_walk_cc(w, d->dtype, st));
   }
   return GLA_OK;
 }
 
-// whether a walk stays in one piece and one segment where `lines` CTAs run
-bool whole(const DecayWalk &w, const gla_decay_desc *d, long lines) {
-  int P, L;
-  plan_segments(d, w.max_len, decay_tc_takes(w, d->dtype), w.K, lines, &P, &L);
-  return w.K <= kPiece && P == 1;
+// Three walks that share nothing, each contraction in one piece: beside each other, split
+// while together they leave SMs idle.  The pre-passes of those that are split come first.
+int run_together(DecayWalk *w, const gla_decay_desc *d, cudaStream_t st) {
+  long lines = 0;
+  for (int i = 0; i < 3; ++i) lines += lines_of(d, w[i].V);
+  bool tc[3], split = false;
+  for (int i = 0; i < 3; ++i) {
+    tc[i] = decay_tc_takes(w[i], d->dtype);
+    plan_segments(d, w[i].max_len, tc[i], w[i].K, lines, &w[i].P, &w[i].L);
+    w[i].ws = (float *)((char *)w[i].ws + i * ws_states(d));
+    if (w[i].P == 1) continue;
+    w[i].stage = 1;
+    w[i].pre_join = split;
+    GLA_TRY(tc[i] ? decay_walk_tc(w[i], st) : decay_walk_cc(w[i], d->dtype, st));
+    split = true;
+  }
+  for (int i = 0; i < 3; ++i) {
+    w[i].stage = 2;
+    w[i].wait_first = split && i == 0;
+    w[i].settled = split && i > 0;
+    w[i].join = i > 0;
+    w[i].lead = i < 2;
+    GLA_TRY(tc[i] ? decay_walk_tc(w[i], st) : decay_walk_cc(w[i], d->dtype, st));
+  }
+  return GLA_OK;
 }
 
 DecayWalk walk_base(const gla_decay_desc *d, const float *log_decay, const int *cu) {
@@ -601,6 +634,7 @@ DecayWalk walk_base(const gla_decay_desc *d, const float *log_decay, const int *
   w.status = (unsigned *)d->workspace;
   w.ws = (float *)((char *)d->workspace + kStatusBytes);
   w.acc = (float *)((char *)w.ws + ws_states(d));
+  w.stage = 3;
   return w;
 }
 
@@ -618,7 +652,7 @@ extern "C" {
 
 size_t gla_decay_workspace_size(const gla_decay_desc *desc, int for_bwd) {
   if (check_desc(desc) != GLA_OK) return 0;
-  return kStatusBytes + ws_states(desc) + (for_bwd ? ws_acc(desc) : 0);
+  return ws_bytes(desc, for_bwd != 0);
 }
 
 int gla_decay_fwd(const gla_decay_desc *desc, const gla_view *q, const gla_view *k, const gla_view *v,
@@ -665,35 +699,24 @@ int gla_decay_bwd(const gla_decay_desc *desc, const gla_view *q, const gla_view 
   GLA_TRY(check_out(dk, desc, &vdk));
   GLA_TRY(check_out(dv, desc, &vdv));
   cudaStream_t st = (cudaStream_t)stream;
-  const DecayWalk base = walk_base(desc, log_decay, cu_seqlens);
   const int B = desc->B;
-  DecayWalk q_ = base;  // dq = do S^T
-  q_.K = desc->dv, q_.V = desc->dk;
-  q_.x = vdo, q_.y = vv, q_.z = vk, q_.o = vdq;
-  q_.s0 = pool(h0, nullptr, B, desc, true);
-  DecayWalk k_ = base;  // dk = v R^T
-  k_.reverse = 1;
-  k_.K = desc->dv, k_.V = desc->dk;
-  k_.x = vv, k_.y = vdo, k_.z = vq, k_.o = vdk;
-  k_.s0 = pool(dh_final, nullptr, B, desc, true);
-  DecayWalk v_ = base;  // dv = k R, dh0 = lambda R_1
-  v_.reverse = 1;
-  v_.K = desc->dk, v_.V = desc->dv;
-  v_.x = vk, v_.y = vq, v_.z = vdo, v_.o = vdv;
-  v_.s0 = pool(dh_final, nullptr, B, desc, false);
-  v_.s1 = pool(dh0, nullptr, B, desc, false);
-  // The three share nothing but the workspace.  Where together they fill the GPU well enough
-  // to stay whole they use none of it and run side by side.
-  const long all = 2 * lines_of(desc, desc->dk) + lines_of(desc, desc->dv);
-  if (whole(q_, desc, all) && whole(k_, desc, all) && whole(v_, desc, all)) {
-    q_.lead = k_.lead = k_.join = v_.join = 1;
-    GLA_TRY(run_walk(q_, desc, st, all - lines_of(desc, q_.V)));
-    GLA_TRY(run_walk(k_, desc, st, all - lines_of(desc, k_.V)));
-    return run_walk(v_, desc, st, all - lines_of(desc, v_.V));
-  }
-  GLA_TRY(run_walk(q_, desc, st));
-  GLA_TRY(run_walk(k_, desc, st));
-  return run_walk(v_, desc, st);
+  DecayWalk w[3];
+  for (DecayWalk &x : w) x = walk_base(desc, log_decay, cu_seqlens);
+  w[0].K = desc->dv, w[0].V = desc->dk;  // dq = do S^T
+  w[0].x = vdo, w[0].y = vv, w[0].z = vk, w[0].o = vdq;
+  w[0].s0 = pool(h0, nullptr, B, desc, true);
+  w[1].reverse = 1;  // dk = v R^T
+  w[1].K = desc->dv, w[1].V = desc->dk;
+  w[1].x = vv, w[1].y = vdo, w[1].z = vq, w[1].o = vdk;
+  w[1].s0 = pool(dh_final, nullptr, B, desc, true);
+  w[2].reverse = 1;  // dv = k R, dh0 = lambda R_1
+  w[2].K = desc->dk, w[2].V = desc->dv;
+  w[2].x = vk, w[2].y = vq, w[2].z = vdo, w[2].o = vdv;
+  w[2].s0 = pool(dh_final, nullptr, B, desc, false);
+  w[2].s1 = pool(dh0, nullptr, B, desc, false);
+  if (desc->dv <= kPiece) return run_together(w, desc, st);
+  for (const DecayWalk &x : w) GLA_TRY(run_walk(x, desc, st));
+  return GLA_OK;
 }
 
 int gla_decay_step(const gla_decay_desc *desc, const gla_view *q, const gla_view *k, const gla_view *v,

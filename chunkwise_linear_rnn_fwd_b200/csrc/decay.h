@@ -42,14 +42,15 @@ struct DecayWalk {
   float *ws;    // [nseq*H][P][K][V]: entry 0 a copy of the start state, entry s the state after segment s-1
   float *acc;   // [H][rows][V] partial outputs of a contraction taken in pieces (rows: nseq * T, or T packed)
   int acc_in, acc_out;  // add the partial outputs to this walk's; write them instead of o
-  // Walks that need nothing of one another run beside each other: `lead` lets the walk
-  // launched next start once all CTAs of this one have, `join` is that next walk, which then
-  // ends no sooner than this one.
-  int lead, join;
-  // The walk of a split call starts beside its pre-pass in the same way, and waits for it
-  // before it reads the states of the segments.
+  // Launches of one call overlap: one with `lead` (every pre-pass) lets the next start once
+  // all its CTAs have, one with `join` (the walk) or `pre_join` (the pre-pass) is such a next
+  // one, which then ends no sooner than the launch ahead of it.  The walk of a split call
+  // waits for its pre-pass before it reads the segments' states; with `settled` all pre-passes
+  // had ended when the walk ahead of it, which has `wait_first`, let it start.
+  int stage;  // 1 the pre-pass of a split walk, 2 the walk, 3 both
+  int lead, join, pre_join, wait_first, settled;
 #ifdef __CUDACC__
-  __host__ __device__ __forceinline__ bool follows() const { return join || P > 1; }
+  __host__ __device__ __forceinline__ bool follows() const { return join || wait_first || P > 1; }
 #endif
   unsigned *status;
 };

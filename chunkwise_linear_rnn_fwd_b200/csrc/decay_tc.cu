@@ -166,7 +166,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const float ld = __ldg(w.ld + h);
   const dev::DSeq sq = dev::decay_seq(w, b);
   const int n = (sq.len + kC - 1) / kC, nseg = max(1, (n + w.L - 1) / w.L);
-  if (seg >= nseg || (!OUT && seg == nseg - 1)) return;  // the whole CTA
+  if (seg >= nseg || (!OUT && seg == nseg - 1)) {  // the whole CTA
+    if (!OUT && w.pre_join && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) dev::pdl_wait();
+    return;
+  }
+  if (OUT && w.wait_first) dev::pdl_wait();
   if (!OUT || w.lead) dev::pdl_launch_dependents();
   const int c_begin = seg * w.L, nloc = max(0, min(n, c_begin + w.L) - c_begin);
   auto chunk_of = [&](int i) { return REV ? n - 1 - (c_begin + i) : c_begin + i; };
@@ -611,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int e = 0; e < kBV; ++e) S[e] = 0.f;
     if (kok) {
       if (OUT && pass) {
-        dev::pdl_wait();
+        if (!w.settled) dev::pdl_wait();
         // entry 0: the start state (segment 0); entries 1 .. seg: states of the segments before
         const float far = (float)dev::decay_pow(rate, (long)w.L * kC);
         for (int j = seg == 0 ? 0 : 1; j <= seg; ++j) {
@@ -730,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   dev::tc_fence_before();
   __syncthreads();
   if (warp == kIssueWarp) dev::tmem_dealloc(tmem, kTmemCols);
-  if (OUT && w.follows() && blockIdx.x == 0 && blockIdx.y == 0) dev::pdl_wait();
+  if ((OUT ? w.follows() : w.pre_join) && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) dev::pdl_wait();
 }
 
 // ---------------------------------------------------------------- host
@@ -769,13 +773,18 @@ int launch(const DecayWalk &w, cudaStream_t st) {
   CUtensorMap mx, my, mz;
   if (!make_map(&mx, w.x, w, w.K) || !make_map(&my, w.y, w, w.K) || !make_map(&mz, w.z, w, w.V)) return GLA_ERR_CUDA;
   const unsigned gx = (unsigned)((long)w.nseq * w.H * ((w.V + kBV - 1) / kBV));
-  if (w.P > 1) {
+  if (w.P > 1 && (w.stage & 1)) {
     // the states of 128 channels do not meet those of the others before the outputs
     constexpr int smem = Smem<1>::bytes + 1024;
     if (const int e = prepare<k_decay_tc<1, false, REV, false>>(smem)) return e;
-    GLA_LAUNCH(K_DECAY_STATES, st,
-               (k_decay_tc<1, false, REV, false><<<dim3(gx, w.P - 1, w.K > 128 ? 2 : 1), kThreads, smem, st>>>(w, mx, my, mz)));
+    const dim3 grid(gx, w.P - 1, w.K > 128 ? 2 : 1);
+    if (w.pre_join)
+      GLA_LAUNCH(K_DECAY_STATES, st,
+                 (void)launch_pdl(k_decay_tc<1, false, REV, false>, grid, dim3(kThreads), smem, st, w, mx, my, mz));
+    else
+      GLA_LAUNCH(K_DECAY_STATES, st, (k_decay_tc<1, false, REV, false><<<grid, kThreads, smem, st>>>(w, mx, my, mz)));
   }
+  if (!(w.stage & 2)) return GLA_OK;
   constexpr int smem = Smem<KB>::bytes + 1024;
   if (const int e = prepare<k_decay_tc<KB, true, REV, ACC>>(smem)) return e;
   if (w.follows())
