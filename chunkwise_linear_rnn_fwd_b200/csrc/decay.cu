@@ -522,17 +522,21 @@ DPool pool(const float *p, const int *idx, int slots, const gla_decay_desc *d, b
                transposed ? (long)d->dv : 1};
 }
 
+// CTAs of the CUDA-core walk that run at once: two an SM fit up to 64 channels (gradients of
+// 4 x 4 heads of 700 tokens of 64 x 64 in fp32: 64 us, 76 if split for one an SM)
+int ctas_cc(int K) { return K <= 64 ? 2 * 148 : 148; }
+
 // Segments per sequence and chunks per segment of a walk.  Splitting reads y and z twice and
-// passes states through memory, so a walk is split only while it leaves SMs idle (148 of
-// them, one CTA a segment and 64 columns).  On tensor cores a chunk of the first pass takes
+// passes states through memory, so a walk is split only while it (or, in a backward, the
+// three together) leaves SMs idle: one CTA a segment and 64 columns, one or two an SM.  On tensor cores a chunk of the first pass takes
 // half the time of one of the second: two segments lose up to 128 channels (4 x 8 heads of
-// 2048 tokens of 128 x 128: 46 us instead of 43) and win above (2 x 4 heads of 16384 of
-// 256 x 512: 386 instead of 533), and segments shorter than four chunks do not pay.  On CUDA
-// cores every split pays (3 x 4 heads of 700 tokens of 64 x 64 in fp32: 148 us whole, 34 by chunks).
+// 2048 tokens of 128 x 128: 43 us instead of 41) and win above (2 x 4 heads of 16384 of
+// 256 x 512: 349 instead of 476), and segments shorter than four chunks do not pay.  On CUDA
+// cores every split pays (3 x 4 heads of 700 tokens of 64 x 64 in fp32: 120 us whole, 29 by chunks).
 long lines_of(const gla_decay_desc *d, int V) { return (long)d->B * d->H * ((V + kBV - 1) / kBV); }
-int most_segments(const gla_decay_desc *d, int max_len, int chunk, long lines, int min_chunks, int least) {
+int most_segments(const gla_decay_desc *d, int max_len, int chunk, long lines, int min_chunks, int least, int ctas) {
   const int n = (max_len + chunk - 1) / chunk;
-  long p = d->segments ? d->segments : 148 / lines;
+  long p = d->segments ? d->segments : ctas / lines;
   if (!d->segments && p > n / min_chunks) p = n / min_chunks;
   if (p > kMaxSegments) p = kMaxSegments;
   if (p > n) p = n;
@@ -541,8 +545,8 @@ int most_segments(const gla_decay_desc *d, int max_len, int chunk, long lines, i
 // lines: CTAs of the unsplit walk
 void plan_segments(const gla_decay_desc *d, int max_len, bool tc, int K, long lines, int *P, int *L) {
   const int chunk = tc ? decay_chunk_tc() : decay_chunk_cc(K);
-  const int p = tc ? most_segments(d, max_len, chunk, lines, 4, K <= 128 ? 3 : 2)
-                   : most_segments(d, max_len, chunk, lines, 1, 2);
+  const int p = tc ? most_segments(d, max_len, chunk, lines, 4, K <= 128 ? 3 : 2, 148)
+                   : most_segments(d, max_len, chunk, lines, 1, 2, ctas_cc(K));
   const int n = (max_len + chunk - 1) / chunk;
   *L = (n + p - 1) / p;
   *P = (n + *L - 1) / *L;
@@ -552,7 +556,8 @@ void plan_segments(const gla_decay_desc *d, int max_len, bool tc, int K, long li
 size_t ws_states(const gla_decay_desc *d) {
   int most = 1;
   for (int V : {d->dk, d->dv}) {
-    const int p = most_segments(d, d->max_len ? d->max_len : d->T, 32, lines_of(d, V), 1, 2);
+    const int K = V == d->dk ? d->dv : d->dk;
+    const int p = most_segments(d, d->max_len ? d->max_len : d->T, 32, lines_of(d, V), 1, 2, ctas_cc(K));
     if (p > most) most = p;
   }
   return most > 1 ? align_up((size_t)d->B * d->H * most * d->dk * d->dv * sizeof(float), 256) : 0;
@@ -597,6 +602,8 @@ int run_walk(DecayWalk w, const gla_decay_desc *d, cudaStream_t st) {
 
 // Three walks that share nothing, each contraction in one piece: beside each other, split
 // while together they leave SMs idle.  The pre-passes of those that are split come first.
+// (4 heads of 8192 tokens of 128 x 256: 111 us; one after another, each split for itself,
+// 199; whole beside each other 239.)
 int run_together(DecayWalk *w, const gla_decay_desc *d, cudaStream_t st) {
   long lines = 0;
   for (int i = 0; i < 3; ++i) lines += lines_of(d, w[i].V);
