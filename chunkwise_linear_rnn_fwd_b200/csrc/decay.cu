@@ -531,7 +531,8 @@ int ctas_cc(int K) { return K <= 64 ? 2 * 148 : 148; }
 // three together) leaves SMs idle: one CTA a segment and 64 columns, one or two an SM.  On tensor cores a chunk of the first pass takes
 // half the time of one of the second: two segments lose up to 128 channels (4 x 8 heads of
 // 2048 tokens of 128 x 128: 43 us instead of 41) and win above (2 x 4 heads of 16384 of
-// 256 x 512: 349 instead of 476), and segments shorter than four chunks do not pay.  On CUDA
+// 256 x 512: 349 instead of 476), and segments of one chunk do not pay (4 heads of 1024 of
+// 128 x 128: 23 us whole, 20 in four segments, 21 in eight).  On CUDA
 // cores every split pays (3 x 4 heads of 700 tokens of 64 x 64 in fp32: 120 us whole, 29 by chunks).
 long lines_of(const gla_decay_desc *d, int V) { return (long)d->B * d->H * ((V + kBV - 1) / kBV); }
 int most_segments(const gla_decay_desc *d, int max_len, int chunk, long lines, int min_chunks, int least, int ctas) {
@@ -545,7 +546,7 @@ int most_segments(const gla_decay_desc *d, int max_len, int chunk, long lines, i
 // lines: CTAs of the unsplit walk
 void plan_segments(const gla_decay_desc *d, int max_len, bool tc, int K, long lines, int *P, int *L) {
   const int chunk = tc ? decay_chunk_tc() : decay_chunk_cc(K);
-  const int p = tc ? most_segments(d, max_len, chunk, lines, 4, K <= 128 ? 3 : 2, 148)
+  const int p = tc ? most_segments(d, max_len, chunk, lines, 2, K <= 128 ? 3 : 2, 148)
                    : most_segments(d, max_len, chunk, lines, 1, 2, ctas_cc(K));
   const int n = (max_len + chunk - 1) / chunk;
   *L = (n + p - 1) / p;
