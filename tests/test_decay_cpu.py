@@ -135,6 +135,7 @@ def test_workspace_size(lib):
     size = lambda for_bwd=0, **kw: lib.gla_decay_workspace_size(ctypes.byref(desc(**kw)), for_bwd)  # noqa: E731
     assert size(B=64, H=16) == 256 == size(1, B=64, H=16)
     assert size(B=1, H=1, T=4096) > 256
+    assert size(1, B=1, H=1, T=4096) - 256 == 3 * (size(B=1, H=1, T=4096) - 256)  # three walks beside each other
     assert size(1, B=64, H=16, dv=512) == 256 + 64 * 300 * 16 * 64 * 4
     assert size(1, B=64, H=16, dv=512, max_len=40) == 256 + 300 * 16 * 64 * 4  # T rows in all
     for max_len in range(1, 2000, 37):  # a shorter bound never needs more
