@@ -115,6 +115,13 @@ __device__ __forceinline__ void st_global_32(void *p, const uint32_t *w) {
                : "memory");
 }
 
+__device__ __forceinline__ void ld_global_32(const float *p, float *x) {
+  asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+               : "l"(p)
+               : "memory");
+}
+
 // ACC: a contraction taken in pieces, with partial outputs read or written
 template <int KB, bool OUT, bool REV, bool ACC>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -631,7 +638,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (seg == 0) {
         if (i0 >= 0) {
           const float *u = w.s0.p + i0 * w.s0.slot + h * w.s0.head + kr * w.s0.row + v0 * w.s0.col;
-          if (w.s0.col == 1) {
+          if (w.s0.col == 1 && ((uintptr_t)u & 31u) == 0) {
+#pragma unroll
+            for (int e = 0; e < kBV; e += 8)
+              if (e < nv) ld_global_32(u + e, S + e);
+          } else if (w.s0.col == 1) {
 #pragma unroll
             for (int e = 0; e < kBV; e += 4)
               if (e < nv) {
@@ -715,7 +726,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<float4 *>(wsb + (seg + 1) * KV + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
       } else if (last && i1 >= 0) {
         float *u = w.s1.p + i1 * w.s1.slot + h * w.s1.head + kr * w.s1.row + v0 * w.s1.col;
-        if (w.s1.col == 1) {
+        if (w.s1.col == 1 && ((uintptr_t)u & 31u) == 0) {
+#pragma unroll
+          for (int e = 0; e < kBV; e += 8)
+            if (e < nv) st_global_32(u + e, reinterpret_cast<const uint32_t *>(S + e));
+        } else if (w.s1.col == 1) {
 #pragma unroll
           for (int e = 0; e < kBV; e += 4)
             if (e < nv) *reinterpret_cast<float4 *>(u + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);

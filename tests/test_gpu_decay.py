@@ -194,6 +194,20 @@ def test_pool_in_place(dtype, segments):
     assert torch.equal(pool[2], before[2])  # an empty sequence passes its state on
 
 
+@pytest.mark.parametrize("offset", [4, 8])
+def test_pools_aligned_to_16_or_32_bytes(offset):
+    """States are moved 32 bytes at a time where their address allows, 16 elsewhere."""
+    b = Batch([200, 31], 2, 64, 72, BF16, seed=71)
+    x = views(b, ("q", "k", "v"), "tokens")
+    h0, hT = (torch.full((b.h0.numel() + 64,), 7.0, device="cuda") for _ in range(2))
+    h0v, hTv = (t[offset:offset + b.h0.numel()].view(b.h0.shape) for t in (h0, hT))
+    assert h0v.data_ptr() % 32 == (4 * offset) % 32
+    h0v.copy_(b.h0)
+    o, _ = pkg.gla_decay_fwd(x["q"], x["k"], x["v"], b.ld.cuda(), h0=h0v, h_final=hTv, **packing(b, "tokens"))
+    check({"o": rows(o), "h_final": hTv}, reference(b), b, True)
+    assert torch.all(hT[:offset] == 7) and torch.all(hT[offset + b.h0.numel():] == 7)
+
+
 def test_pool_conflicts_are_reported():
     """One entry named twice, another sequence's entry read, an entry past the pool."""
     b = Batch([150, 40, 20], 1, 64, 64, BF16, seed=12)
