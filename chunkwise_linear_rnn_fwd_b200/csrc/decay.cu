@@ -2,6 +2,7 @@
 // chunked walk on CUDA cores and the recurrent step.
 #include "decay.h"
 
+#include "decay_plan.h"
 #include "tc_common.cuh"
 
 namespace gla {
@@ -36,7 +37,7 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
 // fp32 arithmetic and shared-memory reads, not by HBM.
 // ============================================================================
 constexpr int kThreads = 256;
-constexpr int kBV = 64;
+constexpr int kBV = kDecayTileV;
 
 template <int C, int K>
 struct CcSmem {
@@ -471,8 +472,6 @@ int step(const gla_decay_desc &d, const DView &q, const DView &k, const DView &v
 
 }  // namespace
 
-int decay_chunk_cc(int K) { return K <= 128 ? 64 : 32; }
-
 int decay_walk_cc(const DecayWalk &w, int dtype, cudaStream_t st) {
   if (w.reverse) return dtype == GLA_DTYPE_BF16 ? walk_cc<__nv_bfloat16, true>(w, st) : walk_cc<float, true>(w, st);
   return dtype == GLA_DTYPE_BF16 ? walk_cc<__nv_bfloat16, false>(w, st) : walk_cc<float, false>(w, st);
@@ -486,8 +485,6 @@ namespace {
     if (_r != GLA_OK) return _r; \
   } while (0)
 
-constexpr int kPiece = 256;        // channels of one contraction
-constexpr int kMaxSegments = 32;
 constexpr long kMaxHeads = 1 << 20;
 
 int check_desc(const gla_decay_desc *d) {
@@ -495,7 +492,7 @@ int check_desc(const gla_decay_desc *d) {
   if (d->B < 1 || d->H < 1 || d->T < 1 || d->dk < 1 || d->dv < 1 || d->segments < 0 || d->max_len < 0 ||
       d->max_len > d->T) return GLA_ERR_INVALID_ARG;
   if (d->dtype != GLA_DTYPE_BF16 && d->dtype != GLA_DTYPE_FP32) return GLA_ERR_INVALID_ARG;
-  if (d->dk > 256 || d->dv > 4096 || (long)d->B * d->H > kMaxHeads || d->segments > kMaxSegments)
+  if (d->dk > 256 || d->dv > 4096 || (long)d->B * d->H > kMaxHeads || d->segments > kDecayMaxSegments)
     return GLA_ERR_UNSUPPORTED_SHAPE;
   return GLA_OK;
 }
@@ -522,56 +519,8 @@ DPool pool(const float *p, const int *idx, int slots, const gla_decay_desc *d, b
                transposed ? (long)d->dv : 1};
 }
 
-// CTAs of the CUDA-core walk that run at once: two an SM fit up to 64 channels (gradients of
-// 4 x 4 heads of 700 tokens of 64 x 64 in fp32: 64 us, 76 if split for one an SM)
-int ctas_cc(int K) { return K <= 64 ? 2 * 148 : 148; }
-
-// Segments per sequence and chunks per segment of a walk.  Splitting reads y and z twice and
-// passes states through memory, so a walk is split only while it (or, in a backward, the
-// three together) leaves SMs idle: one CTA a segment and 64 columns, one or two an SM.  On tensor cores a chunk of the first pass takes
-// half the time of one of the second: two segments lose up to 128 channels (4 x 8 heads of
-// 2048 tokens of 128 x 128: 43 us instead of 41) and win above (2 x 4 heads of 16384 of
-// 256 x 512: 349 instead of 476), and segments of one chunk do not pay (4 heads of 1024 of
-// 128 x 128: 23 us whole, 20 in four segments, 21 in eight).  On CUDA
-// cores every split pays (3 x 4 heads of 700 tokens of 64 x 64 in fp32: 120 us whole, 29 by chunks).
-long lines_of(const gla_decay_desc *d, int V) { return (long)d->B * d->H * ((V + kBV - 1) / kBV); }
-int most_segments(const gla_decay_desc *d, int max_len, int chunk, long lines, int min_chunks, int least, int ctas) {
-  const int n = (max_len + chunk - 1) / chunk;
-  long p = d->segments ? d->segments : ctas / lines;
-  if (!d->segments && p > n / min_chunks) p = n / min_chunks;
-  if (p > kMaxSegments) p = kMaxSegments;
-  if (p > n) p = n;
-  return p < 1 || (!d->segments && p < least) ? 1 : (int)p;
-}
-// lines: CTAs of the unsplit walk
-void plan_segments(const gla_decay_desc *d, int max_len, bool tc, int K, long lines, int *P, int *L) {
-  const int chunk = tc ? decay_chunk_tc() : decay_chunk_cc(K);
-  const int p = tc ? most_segments(d, max_len, chunk, lines, 2, K <= 128 ? 3 : 2, 148)
-                   : most_segments(d, max_len, chunk, lines, 1, 2, ctas_cc(K));
-  const int n = (max_len + chunk - 1) / chunk;
-  *L = (n + p - 1) / p;
-  *P = (n + *L - 1) / *L;
-}
-
-// bytes of ws: the state copies of the walk that needs most, whatever path it takes
-size_t ws_states(const gla_decay_desc *d) {
-  int most = 1;
-  for (int V : {d->dk, d->dv}) {
-    const int K = V == d->dk ? d->dv : d->dk;
-    const int p = most_segments(d, d->max_len ? d->max_len : d->T, 32, lines_of(d, V), 1, 2, ctas_cc(K));
-    if (p > most) most = p;
-  }
-  return most > 1 ? align_up((size_t)d->B * d->H * most * d->dk * d->dv * sizeof(float), 256) : 0;
-}
-// partial outputs of a backward whose contraction over dv is taken in pieces
-size_t ws_acc(const gla_decay_desc *d) {
-  const size_t rows = d->max_len ? (size_t)d->T : (size_t)d->B * d->T;
-  return d->dv > kPiece ? align_up(rows * d->H * d->dk * sizeof(float), 256) : 0;
-}
-
-// The three walks of a backward, unless they need ws_acc, run together: states for each.
 size_t ws_bytes(const gla_decay_desc *d, bool bwd) {
-  return kStatusBytes + ws_states(d) * (bwd && d->dv <= kPiece ? 3 : 1) + (bwd ? ws_acc(d) : 0);
+  return kStatusBytes + decay_states_areas(d, bwd) * decay_states_bytes(d) + (bwd ? decay_acc_bytes(d) : 0);
 }
 
 int check_ws(const gla_decay_desc *d, bool bwd) {
@@ -581,21 +530,21 @@ int check_ws(const gla_decay_desc *d, bool bwd) {
   return GLA_OK;
 }
 
-// One walk by itself, its contraction over K channels in pieces of at most kPiece.
+// One walk by itself, its contraction over K channels in pieces of at most kDecayPiece.
 int run_walk(DecayWalk w, const gla_decay_desc *d, cudaStream_t st) {
   const int K = w.K;
   const long es = d->dtype == GLA_DTYPE_BF16 ? 2 : 4;
   char *const x = (char *)w.x.p, *const y = (char *)w.y.p;
   float *const s0 = w.s0.p;
   const bool tc = decay_tc_takes(w, d->dtype);
-  for (int k0 = 0; k0 < K; k0 += kPiece) {
-    w.K = K - k0 < kPiece ? K - k0 : kPiece;
+  for (int k0 = 0; k0 < K; k0 += kDecayPiece) {
+    const DecaySplit p = decay_split(d, tc, K, k0, w.V, decay_lines(d, w.V));
+    w.K = p.K, w.P = p.P, w.L = p.L;
     w.x.p = x + k0 * es;
     w.y.p = y + k0 * es;
     if (s0) w.s0.p = s0 + k0 * w.s0.row;
     w.acc_in = k0 > 0;
-    w.acc_out = k0 + kPiece < K;
-    plan_segments(d, w.max_len, tc, w.K, lines_of(d, w.V), &w.P, &w.L);
+    w.acc_out = k0 + kDecayPiece < K;
     GLA_TRY(tc ? decay_walk_tc(w, st) : decay_walk_cc(w, d->dtype, st));
   }
   return GLA_OK;
@@ -607,12 +556,13 @@ int run_walk(DecayWalk w, const gla_decay_desc *d, cudaStream_t st) {
 // 199; whole beside each other 239.)
 int run_together(DecayWalk *w, const gla_decay_desc *d, cudaStream_t st) {
   long lines = 0;
-  for (int i = 0; i < 3; ++i) lines += lines_of(d, w[i].V);
+  for (int i = 0; i < 3; ++i) lines += decay_lines(d, w[i].V);
   bool tc[3], split = false;
   for (int i = 0; i < 3; ++i) {
     tc[i] = decay_tc_takes(w[i], d->dtype);
-    plan_segments(d, w[i].max_len, tc[i], w[i].K, lines, &w[i].P, &w[i].L);
-    w[i].ws = (float *)((char *)w[i].ws + i * ws_states(d));
+    const DecaySplit p = decay_split(d, tc[i], w[i].K, 0, w[i].V, lines);
+    w[i].P = p.P, w[i].L = p.L;
+    w[i].ws = (float *)((char *)w[i].ws + i * decay_states_bytes(d));
     if (w[i].P == 1) continue;
     w[i].stage = 1;
     w[i].pre_join = split;
@@ -641,7 +591,7 @@ DecayWalk walk_base(const gla_decay_desc *d, const float *log_decay, const int *
   w.cu = cu;
   w.status = (unsigned *)d->workspace;
   w.ws = (float *)((char *)d->workspace + kStatusBytes);
-  w.acc = (float *)((char *)w.ws + ws_states(d));
+  w.acc = (float *)((char *)w.ws + decay_states_bytes(d));
   w.stage = 3;
   return w;
 }
@@ -722,7 +672,7 @@ int gla_decay_bwd(const gla_decay_desc *desc, const gla_view *q, const gla_view 
   w[2].x = vk, w[2].y = vq, w[2].z = vdo, w[2].o = vdv;
   w[2].s0 = pool(dh_final, nullptr, B, desc, false);
   w[2].s1 = pool(dh0, nullptr, B, desc, false);
-  if (desc->dv <= kPiece) return run_together(w, desc, st);
+  if (desc->dv <= kDecayPiece) return run_together(w, desc, st);
   for (const DecayWalk &x : w) GLA_TRY(run_walk(x, desc, st));
   return GLA_OK;
 }

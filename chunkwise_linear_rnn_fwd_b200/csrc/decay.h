@@ -59,8 +59,6 @@ struct DecayWalk {
 int decay_walk_cc(const DecayWalk &w, int dtype, cudaStream_t st);
 bool decay_tc_takes(const DecayWalk &w, int dtype);
 int decay_walk_tc(const DecayWalk &w, cudaStream_t st);
-int decay_chunk_tc();
-int decay_chunk_cc(int K);
 
 #ifdef __CUDACC__
 namespace dev {

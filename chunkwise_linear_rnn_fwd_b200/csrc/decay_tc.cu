@@ -43,14 +43,15 @@
 // scaling and of the scores cost more in instruction misses than they save (132 us against
 // 94 at one size); two and three issuing warps were slower than one.
 #include "decay.h"
+#include "decay_plan.h"
 #include "tc_common.cuh"
 #include "tc_path.h"
 
 namespace gla {
 namespace {
 
-constexpr int kC = 128;   // tokens of a chunk
-constexpr int kBV = 64;   // columns of V per CTA
+constexpr int kC = decay_chunk_tc();  // tokens of a chunk
+constexpr int kBV = kDecayTileV;      // columns of V per CTA
 constexpr int kThreads = 512;
 constexpr int kTmemCols = 512;
 // TMEM columns: scores fp32 (then P in bf16), the output accumulators, dS (64 columns for
@@ -811,8 +812,6 @@ int launch(const DecayWalk &w, cudaStream_t st) {
 }
 
 }  // namespace
-
-int decay_chunk_tc() { return kC; }
 
 bool decay_tc_takes(const DecayWalk &w, int dtype) {
   return dtype == GLA_DTYPE_BF16 && w.K % 8 == 0 && w.V % 8 == 0 && ok_view(w.x, w) && ok_view(w.y, w) &&
