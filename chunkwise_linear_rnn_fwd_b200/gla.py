@@ -546,19 +546,23 @@ def _on_device(fn):
     """_on_stream, on the device of the first tensor: the library launches on the device
     that is current, so a call with tensors of another device makes that one current."""
     on_stream = _on_stream(fn)
+    first = fn.__code__.co_varnames[0]
 
     @functools.wraps(fn)
-    def wrapper(x, *args, **kwargs):
+    def wrapper(*args, **kwargs):
+        x = args[0] if args else kwargs.get(first)
+        if x is None:
+            return fn(*args, **kwargs)  # which names what is missing
         index = x.get_device()
         if index < 0:
             raise ValueError("tensors passed to the GLA library must be on a CUDA device")
         stream = kwargs.get("stream")
         if stream is None and index == torch._C._cuda_getDevice():
-            return fn(x, *args, **kwargs)
+            return fn(*args, **kwargs)
         if stream is not None and stream.device != x.device:
             raise ValueError("stream and tensors are on different devices")
         with torch.cuda.device(index):
-            return on_stream(x, *args, **kwargs)
+            return on_stream(*args, **kwargs)
     return wrapper
 
 
