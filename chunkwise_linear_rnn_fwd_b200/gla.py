@@ -668,7 +668,8 @@ def gla_decay_fwd(q, k, v, log_decay, *, cu_seqlens=None, max_len=None, h0=None,
     q, k [B,H,T,dk], v [B,H,T,dv] with any distances between sequences, heads and tokens (a
     transposed view of token-major rows is fine, and one expanded over heads); log_decay [H] fp32.  Dense: B sequences of T
     tokens.  Packed: cu_seqlens [n+1] int32, B = 1, sequence i owns rows cu[i] .. cu[i+1]-1 and
-    none is longer than max_len; rows of no sequence are left as they are in `o`.
+    none is longer than max_len; rows of no sequence are left as they are in a given `o` and are
+    zero in one that the call makes.
     h0 [slots,H,dk,dv] fp32: start states, sequence i from entry h0_index[i] (int32; default i;
     negative: zero).  h_final: where the last states go, by h_final_index (negative: nowhere);
     it may be h0 itself.  Without it, and with want_final, a new [n,H,dk,dv] tensor."""
@@ -677,7 +678,8 @@ def gla_decay_fwd(q, k, v, log_decay, *, cu_seqlens=None, max_len=None, h0=None,
     dv = v.shape[-1]
     index, dt, f32, i32 = q.get_device(), q.dtype, torch.float32, torch.int32
     if o is None:
-        o = torch.empty(B, H, T, dv, dtype=dt, device=q.device)
+        # rows of no sequence are not written
+        o = (torch.empty if cu_seqlens is None else torch.zeros)(B, H, T, dv, dtype=dt, device=q.device)
     if h_final is None and h_final_index is not None:
         raise ValueError("h_final_index needs h_final")
     slots0, slots1 = (0 if h0 is None else h0.shape[0]), (None if h_final is None else h_final.shape[0])
@@ -701,13 +703,21 @@ def gla_decay_bwd(q, k, v, log_decay, do, *, cu_seqlens=None, max_len=None, h0=N
     """Backward of gla_decay_fwd: (dq, dk, dv, dh0 or None) from do [B,H,T,dv] and dh_final
     [n,H,dk,dv] (None: zero); h0 [n,H,dk,dv] or None, in order.  The decay is a constant.
     An input expanded over heads or sequences gets a gradient for each: sum them.
-    See include/gla.h."""
+    Rows of no sequence: as in gla_decay_fwd.  See include/gla.h."""
     lib = load()
     B, H, T, K = q.shape
     V = v.shape[-1]
     index, dt, f32 = q.get_device(), q.dtype, torch.float32
     n, cu, d, workspace = _decay_setup(q, v, index, cu_seqlens, max_len, 0, 0, segments, workspace, 1)
-    dq, dk, dv = (torch.empty_like(like) if t is None else t for t, like in ((dq, q), (dk, k), (dv, v)))
+    made = []
+    if dq is None:
+        made.append(dq := torch.empty_like(q))
+    if dk is None:
+        made.append(dk := torch.empty_like(k))
+    if dv is None:
+        made.append(dv := torch.empty_like(v))
+    if cu is not None and made:
+        torch._foreach_zero_(made)  # rows of no sequence are not written; one launch for the three
     if dh0 is None and want_dh0:
         dh0 = torch.empty(n, H, K, V, dtype=f32, device=q.device)
     sk, sv, ss = q.shape, (B, H, T, V), (n, H, K, V)

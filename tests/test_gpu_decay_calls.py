@@ -30,3 +30,33 @@ def test_keywords_give_what_positions_give():
     fwd = pkg.gla_layernorm_fwd(x=r)
     same(fwd, pkg.gla_layernorm_fwd(r))
     same(pkg.gla_layernorm_bwd(x=r, dy=r, mean=fwd[1], rstd=fwd[2]), pkg.gla_layernorm_bwd(r, r, *fwd[1:]))
+
+
+def poison(nbytes):
+    """Leaves NaN in the memory that the next allocations of this size get."""
+    x = torch.full((nbytes // 4,), float("nan"), device="cuda")
+    torch.cuda.synchronize()
+    del x
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 64), (F32, 64), (BF16, 33)])
+@pytest.mark.parametrize("given", [(), ("dk",)])
+def test_rows_of_no_sequence_are_zero_in_outputs_the_call_makes(dtype, d, given):
+    """Rows before the first sequence, behind the last one, and those of a sequence that is
+    refused; whatever the memory held."""
+    b = Batch([40, 700, 30], 2, d, d, dtype, seed=3, spare=300)
+    x, ld = views(b, ("q", "k", "v", "do"), "tokens"), b.ld.cuda()
+    q, k, v, do = (x[n] for n in ("q", "k", "v", "do"))
+    cu = torch.tensor([7, 40, 740, 770], dtype=torch.int32, device="cuda")
+    nobody = torch.ones(b.rows, dtype=torch.bool, device="cuda")
+    nobody[7:40] = nobody[740:770] = False  # the second sequence is longer than max_len
+    p = {"cu_seqlens": cu, "max_len": 300}
+    poison(q.numel() * q.element_size())
+    o, _ = pkg.gla_decay_fwd(q, k, v, ld, want_final=False, **p)
+    for _ in range(3):
+        poison(q.numel() * q.element_size())
+    mine = {n: torch.full_like(q, 7.0) for n in given}
+    g = dict(zip(("dq", "dk", "dv"), pkg.gla_decay_bwd(q, k, v, ld, do, want_dh0=False, **mine, **p)))
+    for name, t in {"o": o, **g}.items():
+        assert bool((t[0][:, nobody] == (7.0 if name in given else 0.0)).all()), name
+        assert bool(torch.isfinite(t).all()) and bool((t[0][:, ~nobody] != 0.0).any())
