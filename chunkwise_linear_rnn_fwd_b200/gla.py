@@ -587,6 +587,13 @@ def _dense(t, name, dtype, shape, index):
     return t.data_ptr()
 
 
+def _workspace(ws, index):
+    """(address, bytes) of a workspace: contiguous memory of the device that the call runs on."""
+    if ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"workspace: expected contiguous memory on cuda:{index}, got strides {ws.stride()} on {ws.device}")
+    return ws.data_ptr(), ws.nbytes
+
+
 def _views(dtype, index, *tensors):
     """gla_view of each (tensor [B,H,T,d] or, one token, [B,H,d], its name, its shape): an array of
     them, and the address of the first (they lie 32 bytes apart)."""
@@ -601,14 +608,13 @@ def _views(dtype, index, *tensors):
     return a, a.buffer_info()[0]
 
 
-def _decay_desc(B, H, T, max_len, dk, dv, dtype, slots0=0, slots1=0, segments=0, workspace=None) -> gla_decay_desc:
+def _decay_desc(B, H, T, max_len, dk, dv, dtype, slots0=0, slots1=0, segments=0, workspace=None,
+                index=0) -> gla_decay_desc:
     code = DTYPE.get(dtype)
     if code is None:
         raise ValueError(f"unsupported dtype {dtype}")
-    if workspace is None:
-        return gla_decay_desc(B, H, T, max_len, dk, dv, code, slots0, slots1, segments, None, 0)
-    return gla_decay_desc(B, H, T, max_len, dk, dv, code, slots0, slots1, segments, workspace.data_ptr(),
-                          workspace.nbytes)
+    ws, size = (None, 0) if workspace is None else _workspace(workspace, index)
+    return gla_decay_desc(B, H, T, max_len, dk, dv, code, slots0, slots1, segments, ws, size)
 
 
 def decay_workspace_size(B, H, T, dk, dv, dtype, for_bwd=False, *, max_len=0, segments=0) -> int:
@@ -651,7 +657,7 @@ def _decay_setup(q, v, index, cu_seqlens, max_len, slots0, slots1, segments, wor
         B = cu_seqlens.numel() - 1
         cu = _dense(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), index)
     d = _decay_desc(B, H, T, max_len, dk, v.shape[-1], q.dtype, B if slots0 is None else slots0,
-                    B if slots1 is None else slots1, segments, workspace)
+                    B if slots1 is None else slots1, segments, workspace, index)
     if workspace is None:
         n = _decay_bytes(B, H, T, max_len, dk, v.shape[-1], q.dtype, segments, for_bwd)
         workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
@@ -743,7 +749,7 @@ def gla_decay_step(q, k, v, log_decay, state, index=None, *, o=None, workspace=N
     if o is None:
         # a padding row's output is not written
         o = (torch.empty if index is None else torch.zeros)(B, H, dv, dtype=dt, device=q.device)
-    d = _decay_desc(B, H, 1, 0, dk, dv, dt, 0, state.shape[0], 0, workspace)
+    d = _decay_desc(B, H, 1, 0, dk, dv, dt, 0, state.shape[0], 0, workspace, dev)
     keep, p = _views(dt, dev, (q, "q", q.shape), (k, "k", q.shape), (v, "v", (B, H, dv)), (o, "o", (B, H, dv)))
     r = load().gla_decay_step(ctypes.byref(d), p, p + 32, p + 64, _dense(log_decay, "log_decay", f32, (H,), dev),
                               _dense(state, "state", f32, (state.shape[0], H, dk, dv), dev),
@@ -817,7 +823,7 @@ def gla_layernorm_bwd(x, dy, mean, rstd, w=None, *, dx=None, want_dwb=True, work
         if workspace is None:
             workspace = torch.empty(lib.gla_layernorm_workspace_size(rows, n), dtype=torch.uint8, device=x.device)
     (px, ldx), (pg, ldg), (po, ldo) = (_row_view(t, m, x, index) for t, m in ((x, "x"), (dy, "dy"), (dx, "dx")))
-    ws, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    ws, size = (None, 0) if workspace is None else _workspace(workspace, index)
     r = lib.gla_layernorm_bwd(code, rows, n, px, ldx, pg, ldg, _dense(mean, "mean", f32, shape[:-1], index),
                               _dense(rstd, "rstd", f32, shape[:-1], index), _dense(w, "w", f32, (n,), index), po, ldo,
                               pw, pb, ws, size, _raw_stream(stream, index))

@@ -25,3 +25,11 @@ def test_a_missing_argument_is_named():
         pkg.gla_decay_fwd()
     with pytest.raises(TypeError, match="'log_decay'"):
         pkg.gla_decay_step(k=torch.zeros(1), v=torch.zeros(1), state=torch.zeros(1))
+
+
+def test_a_workspace_of_another_device_is_refused():
+    """Its address would go to the kernels of cuda:0."""
+    from chunkwise_linear_rnn_fwd_b200 import gla as G
+    ws = torch.zeros(1024, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="workspace"):
+        G._decay_desc(1, 1, 8, 0, 16, 16, torch.bfloat16, workspace=ws)

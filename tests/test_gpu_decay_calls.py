@@ -60,3 +60,21 @@ def test_rows_of_no_sequence_are_zero_in_outputs_the_call_makes(dtype, d, given)
     for name, t in {"o": o, **g}.items():
         assert bool((t[0][:, nobody] == (7.0 if name in given else 0.0)).all()), name
         assert bool(torch.isfinite(t).all()) and bool((t[0][:, ~nobody] != 0.0).any())
+
+
+def test_workspaces_of_the_host_or_with_gaps_are_refused():
+    b = Batch([20], 2, 64, 64, BF16, seed=4)
+    x, ld, p = views(b, ("q", "k", "v"), "tokens"), b.ld.cuda(), packing(b, "tokens")
+    q, k, v = (x[n] for n in ("q", "k", "v"))
+    tok = [t[0, :, :1].transpose(0, 1) for t in (q, k, v)]
+    r = b.q[:, 0].cuda()
+    _, mean, rstd = pkg.gla_layernorm_fwd(r)
+    calls = [lambda ws: pkg.gla_decay_fwd(q, k, v, ld, workspace=ws, **p),
+             lambda ws: pkg.gla_decay_bwd(q, k, v, ld, v, workspace=ws, **p),
+             lambda ws: pkg.gla_decay_step(*tok, ld, torch.zeros(1, 2, 64, 64, device="cuda"), workspace=ws),
+             lambda ws: pkg.gla_layernorm_bwd(r, r, mean, rstd, workspace=ws)]
+    for call in calls:
+        call(pkg.alloc_decay_workspace(1 << 20, "cuda"))
+        for bad in (torch.zeros(1 << 20, dtype=torch.uint8), torch.zeros(1 << 21, dtype=torch.uint8, device="cuda")[::2]):
+            with pytest.raises(ValueError, match="workspace"):
+                call(bad)
