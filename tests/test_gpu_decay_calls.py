@@ -78,3 +78,33 @@ def test_workspaces_of_the_host_or_with_gaps_are_refused():
         for bad in (torch.zeros(1 << 20, dtype=torch.uint8), torch.zeros(1 << 21, dtype=torch.uint8, device="cuda")[::2]):
             with pytest.raises(ValueError, match="workspace"):
                 call(bad)
+
+
+def carried(state, h0, ld, tokens):
+    """The mean relative error of states [H,..] that only decayed, for each head."""
+    want = h0.double() * torch.exp(ld.double() * tokens).view(-1, *[1] * (h0.dim() - 1))
+    return ((state.double() / want - 1).flatten(1).mean(1)).abs()
+
+
+def mean_bound(updates, values):
+    """What rounding may leave of the mean: each update rounds a value by at most 2^-24 of it, an
+    error of mean zero and at most 2^-24 / sqrt(3) standard deviation.  The errors of one value's
+    updates may all be alike (a value hardly changes from one to the next), those of different
+    values are independent.  Ten standard deviations."""
+    return 10 * 2.0 ** -24 * updates / (3 * values) ** 0.5
+
+
+# rates whose lambda^64 (first) and lambda^128 lie 0.5 steps of fp32 off the next number
+SLOW = (-1.082700009646942e-06, -2.684299943211954e-06)
+
+
+def test_a_slow_head_decays_right_over_a_long_fp32_sequence():
+    """2048 chunks without new tokens: a factor that is off in its last bit would be off the
+    same way in each of them, 6e-5 in all."""
+    T, dk, dv = 131072, 128, 256
+    ld = torch.tensor(SLOW, device="cuda")
+    h0 = 1 + torch.rand(1, 2, dk, dv, generator=torch.Generator().manual_seed(5)).cuda()
+    k, v = torch.zeros(1, 1, T, dk, device="cuda").expand(1, 2, T, dk), torch.zeros(1, 1, T, dv, device="cuda").expand(1, 2, T, dv)
+    o = torch.empty(1, 2, T, dv, device="cuda")
+    _, hT = pkg.gla_decay_fwd(k, k, v, ld, h0=h0, o=o, segments=1)
+    assert bool((carried(hT[0], h0[0], ld, T) <= mean_bound(T // 64, dk * dv)).all())
