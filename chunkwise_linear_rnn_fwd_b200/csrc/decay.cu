@@ -408,7 +408,10 @@ __global__ void __launch_bounds__(256) k_decay_step(int H, int nseq, int K, int 
   float4 x[kBatch];
 #pragma unroll
   for (int j = 0; j < kBatch; ++j) x[j] = load(rg + j * RG);
-  const float lam = (float)dev::decay_pow(dev::decay_rate(__ldg(ld + h), status), 1);
+  // lambda as a sum: one fp32 number is up to 2^-25 off, which is 1 / 90 of what a head of
+  // log lambda = -2.65e-6 forgets a token, and adds up over all of them
+  const double lambda = dev::decay_pow(dev::decay_rate(__ldg(ld + h), status), 1);
+  const float lh = (float)lambda, ll = (float)(lambda - (double)lh);
   if (tid < K) {
     sq[tid] = to_f(((const T *)q.p)[b * q.sb + h * q.sh + tid]);
     sk[tid] = to_f(((const T *)k.p)[b * k.sb + h * k.sh + tid]);
@@ -424,10 +427,10 @@ __global__ void __launch_bounds__(256) k_decay_step(int H, int nseq, int K, int 
       const int r = r0 + j * RG;
       if (r >= K) continue;
       const float kr = sk[r], qr = sq[r];
-      x[j].x = fmaf(lam, x[j].x, kr * vv[0]);
-      x[j].y = fmaf(lam, x[j].y, kr * vv[1]);
-      x[j].z = fmaf(lam, x[j].z, kr * vv[2]);
-      x[j].w = fmaf(lam, x[j].w, kr * vv[3]);
+      x[j].x = fmaf(lh, x[j].x, fmaf(ll, x[j].x, kr * vv[0]));
+      x[j].y = fmaf(lh, x[j].y, fmaf(ll, x[j].y, kr * vv[1]));
+      x[j].z = fmaf(lh, x[j].z, fmaf(ll, x[j].z, kr * vv[2]));
+      x[j].w = fmaf(lh, x[j].w, fmaf(ll, x[j].w, kr * vv[3]));
       acc[0] = fmaf(qr, x[j].x, acc[0]);
       acc[1] = fmaf(qr, x[j].y, acc[1]);
       acc[2] = fmaf(qr, x[j].z, acc[2]);

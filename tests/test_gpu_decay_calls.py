@@ -108,3 +108,13 @@ def test_a_slow_head_decays_right_over_a_long_fp32_sequence():
     o = torch.empty(1, 2, T, dv, device="cuda")
     _, hT = pkg.gla_decay_fwd(k, k, v, ld, h0=h0, o=o, segments=1)
     assert bool((carried(hT[0], h0[0], ld, T) <= mean_bound(T // 64, dk * dv)).all())
+
+
+def test_a_slow_head_decays_right_token_by_token():
+    n, dk, dv = 2000, 128, 256
+    ld = torch.tensor([-2.652400098668295e-06], device="cuda")  # lambda lies half a step of fp32 off
+    h0 = 1 + torch.rand(1, 1, dk, dv, generator=torch.Generator().manual_seed(6)).cuda()
+    k, v, state = torch.zeros(1, 1, dk, device="cuda"), torch.zeros(1, 1, dv, device="cuda"), h0.clone()
+    for _ in range(n):
+        pkg.gla_decay_step(k, k, v, ld, state)
+    assert bool((carried(state[0], h0[0], ld, n) <= mean_bound(n, dk * dv)).all())
