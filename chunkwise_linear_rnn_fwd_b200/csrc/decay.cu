@@ -120,7 +120,9 @@ __global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
   const long KV = (long)w.K * w.V;
   float *wsb = w.ws + bh * w.P * KV;
   const bool pass = w.P > 1 && nseg > 1;  // states come from and go to ws
-  const float far = (float)dev::decay_pow(rate, (long)w.L * C);
+  // lambda^(tokens of a segment) as a sum, like lambda^m below
+  const double across = dev::decay_pow(rate, (long)w.L * C);
+  const float far = (float)across, rest = (float)(across - (double)far);
   if (OUT && pass && !w.settled) dev::pdl_wait();
 #pragma unroll 1
   for (int i = 0; i < K / 64 + (K % 64 ? 1 : 0); ++i)
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
             if (seg == 0) {
               a = u[0];
             } else {
-              for (int j = 1; j <= seg; ++j) a = fmaf(a, far, u[j * KV]);
+              for (int j = 1; j <= seg; ++j) a = fmaf(a, far, fmaf(a, rest, u[j * KV]));
             }
           } else if (seg == 0 && i0 >= 0) {
             a = w.s0.p[i0 * w.s0.slot + h * w.s0.head + k * w.s0.row + vc * w.s0.col];

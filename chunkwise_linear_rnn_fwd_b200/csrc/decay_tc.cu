@@ -625,15 +625,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (OUT && pass) {
         if (!w.settled) dev::pdl_wait();
         // entry 0: the start state (segment 0); entries 1 .. seg: states of the segments before
-        const float far = (float)dev::decay_pow(rate, (long)w.L * kC);
+        // lambda^(tokens of a segment) as a sum, like lambda^m below
+        const double across = dev::decay_pow(rate, (long)w.L * kC);
+        const float far = (float)across, rest = (float)(across - (double)far);
         for (int j = seg == 0 ? 0 : 1; j <= seg; ++j) {
           const float *u = wsb + j * KV;
 #pragma unroll
           for (int e = 0; e < kBV; e += 4)
             if (e < nv) {
               const float4 x = *reinterpret_cast<const float4 *>(u + e);
-              S[e] = fmaf(S[e], far, x.x), S[e + 1] = fmaf(S[e + 1], far, x.y);
-              S[e + 2] = fmaf(S[e + 2], far, x.z), S[e + 3] = fmaf(S[e + 3], far, x.w);
+              S[e] = fmaf(S[e], far, fmaf(S[e], rest, x.x));
+              S[e + 1] = fmaf(S[e + 1], far, fmaf(S[e + 1], rest, x.y));
+              S[e + 2] = fmaf(S[e + 2], far, fmaf(S[e + 2], rest, x.z));
+              S[e + 3] = fmaf(S[e + 3], far, fmaf(S[e + 3], rest, x.w));
             }
         }
       } else if (seg == 0) {

@@ -118,3 +118,15 @@ def test_a_slow_head_decays_right_token_by_token():
     for _ in range(n):
         pkg.gla_decay_step(k, k, v, ld, state)
     assert bool((carried(state[0], h0[0], ld, n) <= mean_bound(n, dk * dv)).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_slow_head_decays_right_across_segments(dtype):
+    """32 segments of 128 tokens: a start state passes 30 joins and at most four chunks."""
+    T, n, dk, dv = 4096, 8, 128, 256
+    ld = torch.tensor(SLOW, device="cuda")
+    h0 = 1 + torch.rand(n, 2, dk, dv, generator=torch.Generator().manual_seed(7)).cuda()
+    k, v = torch.zeros(n, 2, T, dk, dtype=dtype, device="cuda"), torch.zeros(n, 2, T, dv, dtype=dtype, device="cuda")
+    _, hT = pkg.gla_decay_fwd(k, k, v, ld, h0=h0, segments=32)
+    off = carried(hT.transpose(0, 1), h0.transpose(0, 1), ld, T)
+    assert bool((off <= mean_bound(34, n * dk * dv)).all())
