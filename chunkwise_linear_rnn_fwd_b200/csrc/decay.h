@@ -105,7 +105,7 @@ __device__ __forceinline__ void decay_slots(const DPool &s0, const DPool &s1, bo
   i1 = s1.p ? (s1.idx ? __ldg(s1.idx + b) : b) : -1;
   bool bad = false;
   if (i0 >= s0.slots) i0 = -1, bad = s0.p != nullptr;
-  if (i1 >= s1.slots) i1 = -1, bad = true;
+  if (i1 >= s1.slots) i1 = -1, bad |= s1.p != nullptr;
   if (s1.idx || (alias && s0.idx)) {
     int dup = 0, hazard = 0;
     const int me = WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x, all = WARP ? 32 : (int)blockDim.x;

@@ -1,5 +1,7 @@
 """How the decay and layer-norm calls are made on the GPU: arguments by keyword, outputs and
 workspaces that the call makes or is given, states that many chunks and tokens pass on."""
+import ctypes
+
 import pytest
 import torch
 
@@ -130,3 +132,19 @@ def test_a_slow_head_decays_right_across_segments(dtype):
     _, hT = pkg.gla_decay_fwd(k, k, v, ld, h0=h0, segments=32)
     off = carried(hT.transpose(0, 1), h0.transpose(0, 1), ld, T)
     assert bool((off <= mean_bound(34, n * dk * dv)).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_entries_of_a_pool_that_is_not_given_are_not_reported(dtype):
+    """slots0 and slots1 count the entries of pools that are given; without one they mean nothing."""
+    from chunkwise_linear_rnn_fwd_b200 import gla as G
+    b = Batch([20], 2, 64, 64, dtype, seed=8)
+    x, ld = views(b, ("q", "k", "v"), "heads"), b.ld.cuda()
+    o, ws = torch.empty_like(x["v"]), pkg.alloc_decay_workspace(1 << 20, "cuda")
+    d = G._decay_desc(1, 2, 20, 0, 64, 64, dtype, -7, -7, 0, ws, 0)
+    shape = x["q"].shape
+    keep, p = G._views(dtype, 0, *((t, "", shape) for t in (x["q"], x["k"], x["v"], o)))
+    r = pkg.load().gla_decay_fwd(ctypes.byref(d), p, p + 32, p + 64, ld.data_ptr(), None, None, None, p + 96, None, None,
+                                 torch.cuda.current_stream().cuda_stream)
+    assert r == 0 and pkg.poll_status(ws) == 0
+    assert torch.equal(o, pkg.gla_decay_fwd(x["q"], x["k"], x["v"], ld)[0])
