@@ -266,11 +266,12 @@ __global__ void __launch_bounds__(threads_of<G, false>(), ctas_per_sm<VEC, N, G,
   }
 }
 
-// The groups of a backward CTA add up their sums in shared memory; the two groups of rows too
-// wide for that, in the partial sum's own place.
+// The groups of a backward CTA, where it has more than one, add up their sums in shared memory.
 template <int VEC, int N, int G>
 __host__ __device__ constexpr bool sums_in_smem() {
-  return G < threads_of<G, true>() && 2 * VEC * N * G * sizeof(float) <= 40 * 1024;
+  static_assert(G == threads_of<G, true>() || 2 * VEC * N * G * sizeof(float) <= 40 * 1024,
+                "the sums of a CTA with several groups");
+  return G < threads_of<G, true>();
 }
 
 // Thread t of a group carries its columns' sums of dy x^ and dy over all of its rows.
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(threads_of<G, true>(), ctas_per_sm<VEC, N, G, 
     }
   }
   if (!a.part) return;
-  float *part = a.part + (long)blockIdx.x * 2 * a.d, *sums = sums_in_smem<VEC, N, G>() ? shared_sums : part;
+  float *part = a.part + (long)blockIdx.x * 2 * a.d, *sums = shared_sums;
   // the CTA's groups in order
 #pragma unroll 1
   for (int g = 0; g < kGroups; ++g) {
