@@ -44,7 +44,7 @@ struct CcSmem {
   static constexpr int KS = K + 4;
   static constexpr int PS = C + 4;
   static constexpr int x = 0, y = x + C * KS, z = y + C * KS, s = z + C * kBV, p = s + K * kBV, w = p + C * PS;
-  static constexpr int floats = w + C + 1 + 3;
+  static constexpr int wl = w + C + 4, floats = wl + C + 4;
 };
 
 __device__ __forceinline__ float4 load_quad(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
@@ -97,7 +97,7 @@ template <typename T, int C, int K, bool OUT, bool REV>
 __global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
   using L = CcSmem<C, K>;
   extern __shared__ __align__(16) float sm[];
-  float *X = sm + L::x, *Y = sm + L::y, *Z = sm + L::z, *S = sm + L::s, *Pm = sm + L::p, *W = sm + L::w;
+  float *X = sm + L::x, *Y = sm + L::y, *Z = sm + L::z, *S = sm + L::s, *Pm = sm + L::p, *W = sm + L::w, *Wl = sm + L::wl;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int tiles = (w.V + kBV - 1) / kBV;
   const int vt = blockIdx.x % tiles, seg = blockIdx.y;
@@ -114,7 +114,12 @@ __global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
   int i0, i1;
   dev::decay_slots(w.s0, w.s1, w.alias, w.nseq, b, OUT ? w.status : nullptr, i0, i1);
   const double rate = dev::decay_rate(__ldg(w.ld + h), w.status);
-  for (int i = tid; i <= C; i += kThreads) W[i] = (float)dev::decay_pow(rate, i);
+  // lambda^i as W + Wl, W alone where it is not multiplied on
+  for (int i = tid; i <= C; i += kThreads) {
+    const double d = dev::decay_pow(rate, i);
+    W[i] = (float)d;
+    Wl[i] = (float)(d - (double)(float)d);
+  }
 
   // ---- start state: thread (ty, tx) owns rows 4 ty + 64 i + e, columns 4 tx .. +3
   const long KV = (long)w.K * w.V;
@@ -164,8 +169,6 @@ __global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
   const bool wx = OUT && quads(x, w.x.st, w.K), wy = quads(y, w.y.st, w.K), wz = quads(z, w.z.st, nv);
   const long rows = w.packed ? w.T : (long)w.nseq * w.T;
   const int i_end = min(n, (seg + 1) * w.L);
-  int m_of = 0;
-  float dh = 1.f, dl = 0.f;
   for (int i = seg * w.L; i < i_end; ++i) {
     const int c = REV ? n - 1 - i : i;
     const long t0 = (long)c * C;
@@ -266,12 +269,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_cc(DecayWalk w) {
     __syncthreads();
     // lambda^m as a sum: rounded to one fp32 number it is off the same way in every chunk, which
     // a slow head carries on (131072 tokens at log lambda = -1.08e-6: 6.1e-5 of the state, 2e-8 so)
-    if (m != m_of) {
-      const double d = dev::decay_pow(rate, m);
-      dh = (float)d;
-      dl = (float)(d - (double)dh);
-      m_of = m;
-    }
+    const float dh = W[m], dl = Wl[m];
 #pragma unroll 1
     for (int i4 = 0; i4 < (K + 63) / 64; ++i4) {
       const int k0 = 4 * ty + 64 * i4;
