@@ -562,7 +562,7 @@ int run_walk(DecayWalk w, const gla_decay_desc *d, cudaStream_t st) {
 
 // Three walks that share nothing, each contraction in one piece: beside each other, split
 // while together they leave SMs idle.  The pre-passes of those that are split come first.
-// (4 heads of 8192 tokens of 128 x 256: 111 us; one after another, each split for itself,
+// (4 heads of 8192 tokens of 128 x 256: 110 us; one after another, each split for itself,
 // 199; whole beside each other 239.)
 int run_together(DecayWalk *w, const gla_decay_desc *d, cudaStream_t st) {
   long lines = 0;

@@ -19,7 +19,7 @@ constexpr int decay_chunk_tc() { return 128; }
 inline int decay_chunk_cc(int K) { return K <= 128 ? 64 : 32; }
 
 // CTAs of the CUDA-core walk that run at once: two an SM fit up to 64 channels (gradients of
-// 4 x 4 heads of 700 tokens of 64 x 64 in fp32: 64 us, 76 if split for one an SM).  Counted for
+// 4 x 4 heads of 700 tokens of 64 x 64 in fp32: 66 us, 76 if split for one an SM).  Counted for
 // the whole contraction, not for its last and perhaps narrow piece: all pieces of a walk share
 // one area for their states.
 inline int decay_ctas_cc(int whole) { return whole <= 64 ? 2 * 148 : 148; }
@@ -35,11 +35,11 @@ inline int decay_max_len(const gla_decay_desc *d) { return d->max_len ? d->max_l
 // passes states through memory, so a walk is split only while it (or, in a backward, the
 // three together) leaves SMs idle: one CTA a segment and 64 columns, one or two an SM.  On
 // tensor cores a chunk of the first pass takes half the time of one of the second: two
-// segments lose up to 128 channels (4 x 8 heads of 2048 tokens of 128 x 128: 43 us instead of
-// 41) and win above (2 x 4 heads of 16384 of 256 x 512: 349 instead of 476), and segments of
+// segments lose up to 128 channels (4 x 8 heads of 2048 tokens of 128 x 128: 44 us instead of
+// 43) and win above (2 x 4 heads of 16384 of 256 x 512: 348 instead of 476), and segments of
 // one chunk do not pay (4 heads of 1024 of 128 x 128: 23 us whole, 20 in four segments, 21 in
-// eight).  On CUDA cores every split pays (3 x 4 heads of 700 tokens of 64 x 64 in fp32: 120 us
-// whole, 29 by chunks).
+// eight).  On CUDA cores every split pays (3 x 4 heads of 700 tokens of 64 x 64 in fp32: 121 us
+// whole, 30 by chunks).  All of these from captured graphs, with states read and written.
 inline int decay_most_segments(const gla_decay_desc *d, int chunk, long lines, int min_chunks, int least, int ctas) {
   const int n = (decay_max_len(d) + chunk - 1) / chunk;
   long p = d->segments ? d->segments : ctas / lines;

@@ -643,7 +643,7 @@ def _decay_bytes(B, H, T, max_len, dk, dv, dtype, segments, for_bwd) -> int:
 
 def _decay_setup(q, v, index, cu_seqlens, max_len, slots0, slots1, segments, workspace, for_bwd):
     """(B sequences, cu pointer, descriptor, workspace) of a chunked call.  A workspace the
-    caller did not pass lives for this call; nobody reads its status word."""
+    caller did not pass lives for this call, and its status word, never cleared, is not read."""
     B, H, T, dk = q.shape
     if cu_seqlens is None:
         if max_len is not None:
@@ -678,7 +678,10 @@ def gla_decay_fwd(q, k, v, log_decay, *, cu_seqlens=None, max_len=None, h0=None,
     zero in one that the call makes.
     h0 [slots,H,dk,dv] fp32: start states, sequence i from entry h0_index[i] (int32; default i;
     negative: zero).  h_final: where the last states go, by h_final_index (negative: nowhere);
-    it may be h0 itself.  Without it, and with want_final, a new [n,H,dk,dv] tensor."""
+    it may be h0 itself.  Without it, and with want_final, a new [n,H,dk,dv] tensor.
+    What the device finds (a bad bound, an index out of range or used twice, a positive decay, a
+    wait that ran out) is reported in the status word of a workspace that the caller passes
+    (alloc_decay_workspace, poll_status), and nowhere without one."""
     lib = load()
     B, H, T, dk = q.shape
     dv = v.shape[-1]
@@ -709,7 +712,7 @@ def gla_decay_bwd(q, k, v, log_decay, do, *, cu_seqlens=None, max_len=None, h0=N
     """Backward of gla_decay_fwd: (dq, dk, dv, dh0 or None) from do [B,H,T,dv] and dh_final
     [n,H,dk,dv] (None: zero); h0 [n,H,dk,dv] or None, in order.  The decay is a constant.
     An input expanded over heads or sequences gets a gradient for each: sum them.
-    Rows of no sequence: as in gla_decay_fwd.  See include/gla.h."""
+    Rows of no sequence, and what the device finds: as in gla_decay_fwd.  See include/gla.h."""
     lib = load()
     B, H, T, K = q.shape
     V = v.shape[-1]
@@ -742,7 +745,8 @@ def gla_decay_step(q, k, v, log_decay, state, index=None, *, o=None, workspace=N
     """One token for each of B running sequences of gla_decay_fwd: state [slots,H,dk,dv] fp32 is
     updated in place at entry index[b] (int32; default b; negative: a padding row, left out) and
     o reads it.  q, k [B,H,dk], v [B,H,dv], any distances between rows and heads.  Returns o.
-    workspace: only its status word is used (poll_status).  See include/gla.h."""
+    workspace: only its status word is used (poll_status); without one, what the device finds (an
+    index out of range or used twice, a positive decay) is not reported.  See include/gla.h."""
     B, H, dk = q.shape
     dv = v.shape[-1]
     dev, dt, f32 = q.get_device(), q.dtype, torch.float32

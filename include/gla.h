@@ -319,12 +319,18 @@ int gla_state_scan(const gla_desc *desc, int nseg, int seg, int reverse, const f
  *   packed  (max_len > 0) cu_seqlens [B+1] int32 on the device, not decreasing: sequence b owns the
  *           rows cu_seqlens[b] .. cu_seqlens[b+1]-1 of T rows; sb is ignored.  max_len
  *           (at most T) bounds the longest sequence; a length of zero is allowed.  Rows of
- *           no sequence are neither read nor written.
+ *           no sequence are never written and influence no result, but rows of the tensors
+ *           behind a sequence may be read (up to 127 with its last tile, on tensor cores), so
+ *           nothing else may write them while the call runs.
  *   slots0, slots1: entries of the pools h0 and h_final (at least 1 where those are given).
  *   segments: pieces a long sequence is split into to fill the GPU; 0 = automatic.
  *   dk <= 256, dv <= 4096, B*H <= 2^20.  bf16 tensors whose data and distances are multiples of 16
  *   bytes, with dk and dv multiples of 8 and tokens of their own, run on tcgen05 tensor cores;
- *   every other call runs on CUDA cores (fp32 arithmetic).
+ *   every other call runs on CUDA cores (fp32 arithmetic).  On tensor cores two operands are
+ *   rounded to bf16 on the way to o, dq, dk and dv: a score times its weight, and the state
+ *   that a chunk's tokens read.  Each term of an output is off by up to 2^-8 of itself, as
+ *   much again as the output's own rounding may add; the states and dh0 are not affected.
+ *   fp32 copies of the tensors run without it.
  *   workspace: 256-byte aligned, gla_decay_workspace_size(desc, for_bwd) bytes.
  *   Its first 4 bytes are the status word: zero them once; calls only set bits, and
  *   gla_poll_status reads and clears them (GLA_ERR_TIMEOUT; GLA_ERR_INDEX; GLA_ERR_GATE_RANGE
