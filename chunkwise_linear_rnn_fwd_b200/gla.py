@@ -654,6 +654,7 @@ def _decay_setup(q, v, index, cu_seqlens, max_len, slots0, slots1, segments, wor
             raise ValueError("packed tensors are [1,H,T,d]")
         if max_len is None:
             raise ValueError("packed tensors need max_len, a bound on the longest sequence")
+        max_len = 1 if max_len == 0 else max_len  # a batch of empty sequences; the library's 0 means dense
         B = cu_seqlens.numel() - 1
         cu = _dense(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), index)
     d = _decay_desc(B, H, T, max_len, dk, v.shape[-1], q.dtype, B if slots0 is None else slots0,

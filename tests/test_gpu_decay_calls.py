@@ -148,3 +148,17 @@ def test_entries_of_a_pool_that_is_not_given_are_not_reported(dtype):
                                  torch.cuda.current_stream().cuda_stream)
     assert r == 0 and pkg.poll_status(ws) == 0
     assert torch.equal(o, pkg.gla_decay_fwd(x["q"], x["k"], x["v"], ld)[0])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_batch_of_empty_sequences_passes_its_states_on(dtype):
+    """The longest of no tokens at all is zero."""
+    q = torch.full((1, 2, 6, 64), float("nan"), dtype=dtype, device="cuda")
+    ld, cu = torch.full((2,), -0.5, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda")
+    h = torch.randn(3, 2, 64, 64, generator=torch.Generator().manual_seed(9)).cuda()
+    ws = pkg.alloc_decay_workspace(1 << 20, "cuda")
+    kw = {"cu_seqlens": cu, "max_len": 0, "workspace": ws}
+    o, hT = pkg.gla_decay_fwd(q, q, q, ld, h0=h, **kw)
+    *g, dh0 = pkg.gla_decay_bwd(q, q, q, ld, q, h0=h, dh_final=h, **kw)
+    assert torch.equal(hT, h) and torch.equal(dh0, h) and pkg.poll_status(ws) == 0
+    assert not any(bool(t.any()) for t in (o, *g))
